@@ -63,6 +63,12 @@ typedef int32_t mr_status;
 typedef int32_t mr_dtype;
 #define MR_F32 0
 #define MR_F64 1
+/* Types of the linear-layer operators (rms_norm_forward and below); the
+ * preconditioner's entry points take MR_F32 and MR_F64 only. */
+#define MR_F16 2
+#define MR_BF16 3
+#define MR_E4M3 4 /* 8 bits: 4 exponent, 3 mantissa, largest 448, no infinities    */
+#define MR_E5M2 5 /* 8 bits: 5 exponent, 2 mantissa, largest 57344                 */
 /* Storage flag OR'ed into a state or input dtype (MR_F64 | MR_PACKED):
  * a symmetric d x d matrix kept as its upper triangle packed by rows,
  * element (i, j) with i <= j at offset i*d - i*(i-1)/2 + (j - i), d*(d+1)/2
@@ -496,6 +502,171 @@ mr_status mr_measure_peaks(mr_peak_info* out, void* hip_stream);
  * after it returns; returns the previous cap, or -1 (and changes nothing)
  * for a cap outside [1, 100].  Host-only. */
 int32_t mr_set_jacobi_max_sweeps(int32_t sweeps);
+
+/*
+ * ---- Operators of the linear layers whose weights the step above updates ----
+ *
+ * Forward and backward of what surrounds a weight: the norm before it, the
+ * quantisation of its operands to 8 bits with a float32 scale per block of
+ * 128, the product on such operands, and the products of a bank of expert
+ * weights on rows grouped by expert.  The weight gradients come out in
+ * float32, as gram_ema_update, momentum_ema_batched and precondition_apply
+ * take them.
+ *
+ * The conventions at the top of this file hold (device pointers, row-major,
+ * nothing allocated or waited for, capturable, validation before anything is
+ * enqueued, no output over an input).  One problem per call.  Leading
+ * dimensions are in elements, at most 2^22; row counts may be 0 (then only
+ * what the formula makes of an empty sum is written).  Rows at any alignment
+ * of their type are accepted; rows whose pointers and leading dimensions are
+ * multiples of 16 bytes move in 16-byte units.  Sums are float32; every
+ * output is rounded once, to nearest even.  NaN and infinities propagate to
+ * the outputs that depend on them and to no others.
+ */
+
+/* How scales of an 8-bit matrix (rows x cols) lie: scale of element (i, j) at */
+#define MR_BLOCK_VECTOR 0 /* s[i * lds + j / 128]: 128 consecutive values of a row */
+#define MR_BLOCK_SQUARE 1 /* s[i / 128 * lds + j / 128]: a square of 128 x 128     */
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it and an
+ * 8-bit output after it:
+ *   h = x + residual, rounded to dtype (h = x without a residual),
+ *   rstd_i = (mean_j h_ij^2 + eps)^(-1/2),  y_ij = h_ij rstd_i weight_j,
+ *   scales_ib = max(max_{j in block b} |y_ij|, 2^-100) / F,
+ *   q_ij = y_ij / scales_ib rounded to q_dtype, F = 448 (MR_E4M3) or 57344
+ *   (MR_E5M2); y in float32 before either rounding.
+ * width in [1, 16384].  dtype (x, residual, h, y): MR_F32, MR_F16 or MR_BF16;
+ * w_dtype: dtype or MR_F32.  h is required with a residual and ignored without
+ * one; rstd, y and q (with scales, MR_BLOCK_VECTOR) are each written where not
+ * NULL, at least one of y and q.
+ */
+typedef struct {
+  int64_t rows, width;
+  const void* x;        int64_t ldx;
+  const void* residual; int64_t ldres;
+  const void* weight;
+  void* h;              int64_t ldh;
+  float* rstd;
+  void* y;              int64_t ldy;
+  void* q;              int64_t ldq;
+  float* scales;        int64_t lds;
+  mr_dtype dtype, w_dtype, q_dtype;
+  int32_t reserved;
+  double eps;
+} mr_rms_norm_problem;
+mr_status rms_norm_forward(const mr_rms_norm_problem* problem, void* hip_stream);
+
+/*
+ * Gradient of rms_norm_forward from dy, the gradient of y (of the values that
+ * q stands for, where q is what was used):
+ *   xh = h rstd,  g = dy weight,  dx = dresidual + rstd (g - xh mean_j(g xh)),
+ *   dweight_j = sum_i dy_ij xh_ij (float32).
+ * h and rstd as the forward pass left them (h = x without a residual).
+ * dresidual: the gradient that reaches h by the residual path, or NULL.  dx is
+ * the gradient of x and of the residual alike.  dweight may be NULL.  dtype
+ * covers dy, h, dresidual and dx.  Workspace: rms_norm_backward_workspace
+ * bytes, 256-byte aligned (0 when dweight is NULL).
+ */
+typedef struct {
+  int64_t rows, width;
+  const void* dy;        int64_t lddy;
+  const void* h;         int64_t ldh;
+  const float* rstd;
+  const void* weight;
+  const void* dresidual; int64_t ldres;
+  void* dx;              int64_t lddx;
+  float* dweight;
+  mr_dtype dtype, w_dtype;
+} mr_rms_norm_grad_problem;
+size_t rms_norm_backward_workspace(const mr_rms_norm_grad_problem* problem);
+mr_status rms_norm_backward(const mr_rms_norm_grad_problem* problem, void* ws, size_t ws_bytes, void* hip_stream);
+
+/*
+ * Quantises X (m x n; x_dtype MR_F32, MR_F16 or MR_BF16) to q_dtype (MR_E4M3 or
+ * MR_E5M2) with scales as rms_norm_forward's, in one reading of X:
+ *   Q (m x n) with scales S, blocks along n, and/or
+ *   QT (n x m, the transposed order) with scales ST, blocks along m,
+ * each where its pointer is not NULL (at least one).  block MR_BLOCK_VECTOR: 1
+ * x 128 blocks of Q's and of QT's own rows (S: m x ceil(n/128), ST: n x
+ * ceil(m/128)); MR_BLOCK_SQUARE: 128 x 128 squares, the same in both orders (S:
+ * ceil(m/128) x ceil(n/128), ST its transpose).  A block that holds a NaN or an
+ * infinity stands for NaN throughout.
+ */
+typedef struct {
+  int64_t m, n;
+  const void* X; int64_t ldx;
+  void* Q;       int64_t ldq;
+  float* S;      int64_t lds;
+  void* QT;      int64_t ldqt;
+  float* ST;     int64_t ldst;
+  mr_dtype x_dtype, q_dtype;
+  int32_t block, reserved;
+} mr_quantize_problem;
+mr_status quantize_blocks(const mr_quantize_problem* problem, void* hip_stream);
+
+/*
+ * C = A B^T for 8-bit A (m x k) and B (n x k) with scales per block of 128 of k:
+ *   C_ij = sum_b SA_ib SB_jb sum_{l in block b} A_il B_jl   (+ C_ij, accumulate),
+ * SA and SB as a_block and b_block say.  a_dtype MR_E4M3 or MR_E5M2, b_dtype
+ * MR_E4M3, c_dtype MR_F32, MR_F16 or MR_BF16.  A layer's three products are this one: Y = X
+ * W^T on rows of X and W; dX = dY W on rows of dY and W's transposed copy; dW =
+ * dY^T X on the transposed copies of dY and X.  Workspace:
+ * block_scaled_matmul_workspace bytes (0 for most sizes), 256-byte aligned.
+ */
+typedef struct {
+  int64_t m, n, k;
+  const void* A;   int64_t lda;
+  const float* SA; int64_t ldsa;
+  const void* B;   int64_t ldb;
+  const float* SB; int64_t ldsb;
+  void* C;         int64_t ldc;
+  mr_dtype a_dtype, b_dtype, c_dtype;
+  int32_t a_block, b_block, accumulate;
+} mr_scaled_matmul_problem;
+size_t block_scaled_matmul_workspace(const mr_scaled_matmul_problem* problem);
+mr_status block_scaled_matmul(const mr_scaled_matmul_problem* problem, void* ws, size_t ws_bytes, void* hip_stream);
+
+/*
+ * Products of `rows` rows grouped by expert with the experts' weights W_e (n x
+ * k at W + e * w_stride, leading dimension ldw).  Expert e's rows are r with
+ * offsets[e] <= r < offsets[e + 1]; offsets: experts + 1 device integers of
+ * offset_bits (32 or 64) bits, not decreasing, between 0 and rows.  They are
+ * read on the device only: sizes never reach the host.  (Values outside are
+ * clamped, so nothing out of range is read or written.)
+ *   transpose 0: Y (rows x n), y_r = W_e x_r, X is rows x k
+ *   transpose 1: Y (rows x k), y_r = W_e^T x_r, X is rows x n (the gradient of
+ *                the rows, from that of the outputs)
+ * Rows of no expert get zeros.  dtype (X, W): MR_F16 or MR_BF16; y_dtype: dtype
+ * or MR_F32.
+ */
+typedef struct {
+  int64_t experts, rows, n, k;
+  const void* X; int64_t ldx;
+  const void* W; int64_t ldw, w_stride;
+  const void* offsets;
+  void* Y;       int64_t ldy;
+  mr_dtype dtype, y_dtype;
+  int32_t offset_bits, transpose;
+} mr_grouped_problem;
+mr_status grouped_matmul(const mr_grouped_problem* problem, void* hip_stream);
+
+/*
+ * Gradient of every expert's weight: DW_e = sum over its rows of dy_r x_r^T (n x
+ * k at DW + e * dw_stride), zeros for an expert without rows; plus DW_e with
+ * accumulate.  DY rows x n, X rows x k, dtype MR_F16 or MR_BF16; dw_dtype:
+ * MR_F32 or dtype.
+ */
+typedef struct {
+  int64_t experts, rows, n, k;
+  const void* DY; int64_t lddy;
+  const void* X;  int64_t ldx;
+  const void* offsets;
+  void* DW;       int64_t lddw, dw_stride;
+  mr_dtype dtype, dw_dtype;
+  int32_t offset_bits, accumulate;
+} mr_grouped_grad_problem;
+mr_status grouped_weight_grad(const mr_grouped_grad_problem* problem, void* hip_stream);
 
 const char* mr_status_string(mr_status status);
 const char* mr_last_error_message(void);

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(HERE, "libmatrix_roots.so")
 
 MR_OK = 0
 MR_F32, MR_F64 = 0, 1
+MR_F16, MR_BF16, MR_E4M3, MR_E5M2 = 2, 3, 4, 5
+MR_BLOCK_VECTOR, MR_BLOCK_SQUARE = 0, 1
 MR_LEFT, MR_RIGHT = 1, 2
 MR_NORM_NONE, MR_NORM_TRACE = 0, 1
 MR_AUTO, MR_JACOBI, MR_NEWTON, MR_NEWTON_F64, MR_NEWTON_F32 = 0, 1, 2, 3, 4
@@ -46,6 +48,14 @@ EXPORTED = (
     "hyperball_update_batched_workspace",
     "precondition_apply",
     "precondition_apply_workspace",
+    "rms_norm_forward",
+    "rms_norm_backward",
+    "rms_norm_backward_workspace",
+    "quantize_blocks",
+    "block_scaled_matmul",
+    "block_scaled_matmul_workspace",
+    "grouped_matmul",
+    "grouped_weight_grad",
     "mr_newton_iterations",
     "mr_newton_schedule",
     "mr_measure_peaks",
@@ -87,6 +97,56 @@ class ApplyProblem(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("XL", ctypes.c_void_p), ("ldxl", ctypes.c_int64),
                 ("G", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("XR", ctypes.c_void_p), ("ldxr", ctypes.c_int64),
                 ("U", ctypes.c_void_p), ("ldu", ctypes.c_int64)]
+
+
+class RmsNormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldres", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("rstd", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("lds", ctypes.c_int64), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("q_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
+class RmsNormGradProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dresidual", ctypes.c_void_p), ("ldres", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32)]
+
+
+class QuantizeProblem(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("Q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("S", ctypes.c_void_p), ("lds", ctypes.c_int64),
+                ("QT", ctypes.c_void_p), ("ldqt", ctypes.c_int64), ("ST", ctypes.c_void_p), ("ldst", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ScaledMatmulProblem(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("A", ctypes.c_void_p),
+                ("lda", ctypes.c_int64), ("SA", ctypes.c_void_p), ("ldsa", ctypes.c_int64), ("B", ctypes.c_void_p),
+                ("ldb", ctypes.c_int64), ("SB", ctypes.c_void_p), ("ldsb", ctypes.c_int64), ("C", ctypes.c_void_p),
+                ("ldc", ctypes.c_int64), ("a_dtype", ctypes.c_int32), ("b_dtype", ctypes.c_int32),
+                ("c_dtype", ctypes.c_int32), ("a_block", ctypes.c_int32), ("b_block", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class GroupedProblem(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("Y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("offset_bits", ctypes.c_int32), ("transpose", ctypes.c_int32)]
+
+
+class GroupedGradProblem(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("DY", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("DW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("dw_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("offset_bits", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
 
 
 ROOT_INFO_DTYPE = np.dtype([("scale", "<f8"), ("bound", "<f8"), ("iters", "<i4"), ("fp64_iters", "<i4"),
@@ -150,6 +210,22 @@ def library() -> ctypes.CDLL:
     lib.precondition_apply.restype = i32
     lib.precondition_apply_workspace.argtypes = [vp, i32]
     lib.precondition_apply_workspace.restype = sz
+    lib.rms_norm_forward.argtypes = [vp, vp]
+    lib.rms_norm_forward.restype = i32
+    lib.rms_norm_backward.argtypes = [vp, vp, sz, vp]
+    lib.rms_norm_backward.restype = i32
+    lib.rms_norm_backward_workspace.argtypes = [vp]
+    lib.rms_norm_backward_workspace.restype = sz
+    lib.quantize_blocks.argtypes = [vp, vp]
+    lib.quantize_blocks.restype = i32
+    lib.block_scaled_matmul.argtypes = [vp, vp, sz, vp]
+    lib.block_scaled_matmul.restype = i32
+    lib.block_scaled_matmul_workspace.argtypes = [vp]
+    lib.block_scaled_matmul_workspace.restype = sz
+    lib.grouped_matmul.argtypes = [vp, vp]
+    lib.grouped_matmul.restype = i32
+    lib.grouped_weight_grad.argtypes = [vp, vp]
+    lib.grouped_weight_grad.restype = i32
     lib.mr_newton_iterations.argtypes = [i32, f64, f64]
     lib.mr_newton_iterations.restype = i32
     lib.mr_newton_schedule.argtypes = [f64, vp, i32, vp, vp]
@@ -583,6 +659,6 @@ def trace_enable(on: bool = True) -> bool:
 
 def trace_collect() -> dict:
     """{kernel class: (launches, total_ms)} since the last collect (waits for them)."""
-    recs = (TraceRecord * 32)()
-    k = library().mr_trace_collect(ctypes.addressof(recs), 32)
+    recs = (TraceRecord * 64)()
+    k = library().mr_trace_collect(ctypes.addressof(recs), 64)
     return {recs[i].name.decode(): (int(recs[i].launches), float(recs[i].total_ms)) for i in range(k)}

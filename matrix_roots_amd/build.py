@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmatrix_roots.so")
 SOURCES = ["abi.cpp", "gram.hip", "apply.hip", "root.hip", "jacobi.hip", "cans.hip", "polar.hip", "step.hip",
-           "peaks.hip"]
+           "peaks.hip", "linear.cpp", "norm.hip", "quantize.hip", "scaled.hip", "grouped.hip"]
 ARCH = "gfx950"
 
 # Packed float32 VALU ops are kept out of every code object.

@@ -1,0 +1,152 @@
+// Quantisation of a matrix to 8 bits with a float32 scale per block of 128:
+//
+//   s_b = max(max_{i in b} |x_i|, 2^-100) / F,  q_i = x_i / s_b rounded,
+//
+// b being 128 consecutive columns of a row (and, for the transposed copy, 128
+// consecutive rows of a column) or a square of 128 x 128.  One workgroup per
+// 128 x 128 tile reads it once into registers (8 x 8 values per thread) and
+// writes it in one or both orders; the transposed bytes pass through LDS so
+// that both go out in 128-byte runs.  HBM-bound: nothing is read twice.
+#include "linear_common.hpp"
+#include "mr_common.hpp"
+
+namespace mr {
+
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void quantize_kernel(const QuantArgs a) {
+  __shared__ uint32_t colmax[4][kBlock];
+  __shared__ float colinv[kBlock];
+  __shared__ __align__(16) unsigned char tile[kBlock][kBlock + 16];
+  const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
+  const int across = (a.n + kBlock - 1) / kBlock;
+  const int bx = blockIdx.x % across;      // block of columns
+  const int64_t by = blockIdx.x / across;  // block of rows
+  const int c0 = bx * kBlock;
+  const int64_t r0 = by * kBlock;
+  const int c = c0 + 8 * cg;
+  const int64_t r = r0 + 8 * rg;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    if constexpr (VEC) {
+      if (r + p < a.m && c < a.n) {
+        widen8(load8<T>(x + (r + p) * a.ldx + c), v[p]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = r + p < a.m && c + i < a.n ? widen(x[(r + p) * a.ldx + c + i]) : 0.f;
+    }
+  }
+
+  float square = 0.f;
+  if (a.square) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = umax(m, magnitude(v[p][i]));
+    m = max64(m);
+    if ((t & 63) == 0) colmax[wave][0] = m;
+    __syncthreads();
+    m = umax(umax(colmax[0][0], colmax[1][0]), umax(colmax[2][0], colmax[3][0]));
+    square = block_scale(m, a.e5m2);
+    if (t == 0) {
+      if (a.q) a.s[by * a.lds + bx] = square;
+      if (a.qt) a.st[bx * a.ldst + by] = square;
+    }
+  }
+
+  if (a.q) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float s = square;
+      if (!a.square) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = umax(m, magnitude(v[p][i]));
+        s = block_scale(max16(m), a.e5m2);
+        if (cg == 0 && r + p < a.m) a.s[(r + p) * a.lds + bx] = s;
+      }
+      const float inv = 1.f / s;
+      v2u b;
+      b[0] = pack4(v[p][0] * inv, v[p][1] * inv, v[p][2] * inv, v[p][3] * inv, a.e5m2);
+      b[1] = pack4(v[p][4] * inv, v[p][5] * inv, v[p][6] * inv, v[p][7] * inv, a.e5m2);
+      if (r + p < a.m) {
+        unsigned char* q = a.q + (r + p) * a.ldq + c;
+        if (a.vec_q && c + 8 <= a.n) {
+          *reinterpret_cast<v2u*>(q) = b;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < a.n) q[i] = (unsigned char)(b[i >> 2] >> (8 * (i & 3)));
+        }
+      }
+    }
+  }
+  if (!a.qt) return;
+
+  if (!a.square) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) m = umax(m, magnitude(v[p][i]));
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 32));
+      if ((t & 63) < 16) colmax[wave][8 * cg + i] = m;
+    }
+    __syncthreads();
+    if (t < kBlock) {
+      const float s = block_scale(umax(umax(colmax[0][t], colmax[1][t]), umax(colmax[2][t], colmax[3][t])), a.e5m2);
+      colinv[t] = 1.f / s;
+      if (c0 + t < a.n) a.st[(int64_t)(c0 + t) * a.ldst + by] = s;
+    }
+    __syncthreads();
+  }
+  const float sq_inv = a.square ? 1.f / square : 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float inv = a.square ? sq_inv : colinv[8 * cg + i];
+    v2u b;
+    b[0] = pack4(v[0][i] * inv, v[1][i] * inv, v[2][i] * inv, v[3][i] * inv, a.e5m2);
+    b[1] = pack4(v[4][i] * inv, v[5][i] * inv, v[6][i] * inv, v[7][i] * inv, a.e5m2);
+    *reinterpret_cast<v2u*>(&tile[8 * cg + i][8 * rg]) = b;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int col = 32 * p + (t >> 3), part = 16 * (t & 7);
+    if (c0 + col >= a.n || r0 + part >= a.m) continue;
+    unsigned char* q = a.qt + (int64_t)(c0 + col) * a.ldqt + r0 + part;
+    if (a.vec_qt && r0 + part + 16 <= a.m) {
+      *reinterpret_cast<v4u*>(q) = *reinterpret_cast<const v4u*>(&tile[col][part]);
+    } else {
+      for (int i = 0; i < 16 && r0 + part + i < a.m; ++i) q[i] = tile[col][part + i];
+    }
+  }
+}
+
+hipError_t launch_quantize(const QuantArgs& a, mr_dtype dt, bool vec, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + kBlock - 1) / kBlock * ((a.m + kBlock - 1) / kBlock)));
+#define MR_GO(T)                                                                            \
+  do {                                                                                      \
+    if (vec)                                                                                \
+      hipLaunchKernelGGL((quantize_kernel<T, true>), grid, dim3(256), 0, s, a);             \
+    else                                                                                    \
+      hipLaunchKernelGGL((quantize_kernel<T, false>), grid, dim3(256), 0, s, a);            \
+  } while (0)
+  if (dt == MR_F32)
+    MR_GO(float);
+  else if (dt == MR_F16)
+    MR_GO(_Float16);
+  else
+    MR_GO(bf16_t);
+#undef MR_GO
+  return hipGetLastError();
+}
+
+}  // namespace mr
