@@ -4,10 +4,10 @@
 //   forward    y_r = W_e x_r      P = W_e (along k),        Q = x (along k)
 //   transpose  y_r = W_e^T x_r    P = W_e^T (across n),     Q = x (along n)
 //   weights    DW_e = sum_r dy_r x_r^T
-//                                 P = x (across rows),      Q = dy (across rows)
+//                                 P = dy (across rows),     Q = x (across rows)
 //
-// P is the matrix instruction's row operand, so a lane holds four consecutive
-// outputs of one output row.  Operands whose contraction is not contiguous in
+// P is the matrix instruction's row operand: a lane holds four consecutive
+// rows of P at one row of Q.  Operands whose contraction is not contiguous in
 // memory ("across") go through ds_read_b64_tr_b16, which hands each lane four
 // steps of one column; no transposed copy of a weight is ever made.
 //
@@ -26,6 +26,10 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
+__device__ __forceinline__ void store_once(float v, float* p) { __builtin_nontemporal_store(v, p); }
+__device__ __forceinline__ void store_once(_Float16 v, _Float16* p) { __builtin_nontemporal_store(v, p); }
+__device__ __forceinline__ void store_once(bf16_t v, bf16_t* p) { __builtin_nontemporal_store(v.bits, &p->bits); }
+
 template <typename T>
 __device__ __forceinline__ v16f mfma16(v8s p, v8s q, v16f c);
 template <>
@@ -39,11 +43,11 @@ __device__ __forceinline__ v16f mfma16<bf16_t>(v8s p, v8s q, v16f c) {
 
 // Lane l's part of rows row .. row + 31 at steps 16 ks .. + 15 of a chunk of
 // R-row tile `st`: row l % 32, steps 8 (l / 32) .. + 7.
-template <int R, bool ACROSS>
+template <int R, int UPK, bool ACROSS>
 __device__ __forceinline__ v8s frag16(const unsigned char* st, int row, int ks, int lane) {
   if constexpr (!ACROSS) {
     const int r = row + (lane & 31);
-    return *reinterpret_cast<const v8s*>(st + (r * 8 + dl_slot(r, 2 * ks + (lane >> 5), 8)) * 16);
+    return *reinterpret_cast<const v8s*>(st + (r * UPK + dl_slot(r, 2 * ks + (lane >> 5), UPK)) * 16);
   } else {
     // 16 lanes read four steps x 16 columns (lane i: step i / 4, columns 4 (i % 4) ..)
     // and each gets the four steps of column i
@@ -64,54 +68,85 @@ __device__ __forceinline__ int64_t offset_at(const GroupedArgs& a, int e) {
                                    : (int64_t) reinterpret_cast<const int32_t*>(a.offsets)[e];
   return v < 0 ? 0 : v > a.rows ? a.rows : v;
 }
-// Segment s of the rows: 0 the rows before the first expert, 1 .. E the
-// experts, E + 1 the rows after the last one.
-__device__ __forceinline__ void segment(const GroupedArgs& a, int s, int64_t& begin, int64_t& end) {
-  begin = s == 0 ? 0 : offset_at(a, s - 1);
-  end = s > a.experts ? a.rows : offset_at(a, s);
+// Rows of expert e (none where the offsets decrease).
+__device__ __forceinline__ void expert_rows(const GroupedArgs& a, int e, int64_t& begin, int64_t& end) {
+  begin = offset_at(a, e);
+  end = offset_at(a, e + 1);
   if (end < begin) end = begin;
 }
 
-// Segment and tile within it of tile `id`, BQ rows to a tile, `across` column
-// tiles to a row tile; false past the last one.  Every wave does the same scan.
+// The experts' row tiles, BQ rows to a tile and `across` column tiles to a row
+// tile: each lane counts a run of experts, one scan gives every wave the total
+// and the means to find a tile.
 template <int BQ>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& a, int64_t id, int across, int& seg, int64_t& begin,
-                                          int64_t& end, int& local) {
-  const int lane = threadIdx.x & 63;
-  int64_t base = 0;
-  for (int s0 = 0; s0 < a.experts + 2; s0 += 64) {
-    const int s = s0 + lane;
-    int64_t b = 0, e = 0;
-    if (s < a.experts + 2) segment(a, s, b, e);
-    const int64_t tiles = (e - b + BQ - 1) / BQ * across;
-    int64_t sum = tiles;
+struct RowTiles {
+  int per, mine, sum, total, across;
+  __device__ __forceinline__ int of(const GroupedArgs& a, int e) const {
+    if (e >= a.experts) return 0;
+    int64_t b, t;
+    expert_rows(a, e, b, t);
+    return (int)((t - b + BQ - 1) / BQ) * across;  // all tiles fit a grid
+  }
+  __device__ __forceinline__ void count(const GroupedArgs& a, int across_) {
+    const int lane = threadIdx.x & 63;
+    across = across_;
+    per = (a.experts + 63) / 64;
+    mine = 0;
+    for (int i = 0; i < per; ++i) mine += of(a, lane * per + i);
+    sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t up = __shfl_up(sum, d);
+      const int up = __shfl_up(sum, d);
       if (lane >= d) sum += up;
     }
-    const uint64_t hit = __ballot(id < base + sum);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      seg = s0 + l;
-      begin = __shfl(b, l);
-      end = __shfl(e, l);
-      local = (int)(id - base - (__shfl(sum, l) - __shfl(tiles, l)));
-      return true;
-    }
-    base += __shfl(sum, 63);
+    total = __builtin_amdgcn_readlane(sum, 63);
   }
-  return false;
-}
+  // Expert of tile `id` < total, its rows, and the tile's place among its tiles.
+  __device__ __forceinline__ void find(const GroupedArgs& a, int id, int& e, int64_t& begin, int64_t& end, int& local) const {
+    const uint64_t hit = __ballot(id < sum);
+    const int l = hit ? __builtin_ctzll(hit) : 63;
+    local = id - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l));
+    e = l * per;
+    for (int i = 1; i < per; ++i) {
+      const int t = of(a, e);
+      if (local < t) break;
+      local -= t;
+      ++e;
+    }
+    e = min(e, a.experts - 1);
+    expert_rows(a, e, begin, end);
+  }
+};
+
+// Tiles of a persistent workgroup: tile k of slot b / 8 on XCD b % 8, where
+// every XCD owns one run of `total` / 8 tiles and walks it in order, so that
+// the tiles in flight on an XCD are neighbours and share operands in its L2.
+struct Walk {
+  int at, step, end;
+  __device__ __forceinline__ Walk(int total) {
+    const int x = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
+    end = (int)((int64_t)total * (x + 1) / kNumXcd);
+    at = (int)((int64_t)total * x / kNumXcd) + blockIdx.x / kNumXcd;
+    step = slots;
+  }
+};
 
 }  // namespace
 
-template <int BP_, int BQ_, int WP_, int WQ_>
+// WP x WQ waves multiply, kLoaders waves copy.  NST stages of BK steps in LDS;
+// BPC workgroups to a CU.
+constexpr int kLoaders = 4;
+template <int BP_, int BQ_, int WP_, int WQ_, int BK_, int NST_, int BPC_>
 struct GroupedShape {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NW = WP * WQ, THREADS = 64 * NW;
-  static constexpr int RB = BP / WP / 32, CB = BQ / WQ / 32;
-  static constexpr int P_BYTES = BP * kChunkBytes, STAGE = (BP + BQ) * kChunkBytes;
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NW = WP * WQ, BK = BK_, NST = NST_, BPC = BPC_;
+  static constexpr int THREADS = 64 * (NW + kLoaders);
+  static constexpr int RB = BP / WP / 32, CB = BQ / WQ / 32, KS = BK / 16;
+  static constexpr int P_BYTES = BP * BK * 2, STAGE = (BP + BQ) * BK * 2;
+  static constexpr int COPIES = STAGE / 1024 / kLoaders;  // direct copies per loader wave and chunk
+  static constexpr int SLABS = NST * STAGE;               // where the waves' output slabs start
+  static constexpr int LDS = SLABS + NW * Slab<float>::BYTES;
+  static constexpr int WAVES_PER_SIMD = (BPC * (NW + kLoaders) + 3) / 4;
+  static_assert(KS % 2 == 0 && BPC * LDS <= 160 * 1024, "fragments alternate; the stages fit");
 };
 
 // One operand of a tile: rows (products' rows) r0 .. of `valid`, bytes.
@@ -121,141 +156,356 @@ struct Operand {
   int valid;
 };
 
-// acc = P Q^T over `steps` of the contraction starting at step 0 of both.
-template <class S, typename T, bool PA, bool QA>
-__device__ __forceinline__ void grouped_tile(const Operand& P, const Operand& Q, int64_t steps, bool fast, unsigned char* lds,
-                                             v16f (&acc)[S::RB][S::CB]) {
+// One operand's part of a chunk, by the loader waves.
+template <class S, int R, bool ACROSS>
+__device__ __forceinline__ void stage_operand(const Operand& o, bool direct, bool aligned, int64_t k0, int left,
+                                              unsigned char* st, int loader, int lane) {
+  const int thread = loader * 64 + lane;
+  if constexpr (ACROSS) {
+    if (direct)
+      copy_across<R, kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, loader, lane);
+    else
+      edge_across<R, 64 * kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, aligned, st, thread);
+  } else {
+    if (direct)
+      copy_along<R, kLoaders, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, (left + 7) / 8, st, loader, lane);
+    else
+      edge_along<R, 64 * kLoaders, 2, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, left, aligned, st, thread);
+  }
+}
+
+template <class S>
+struct Frags {
+  v8s p[S::RB], q[S::CB];
+};
+template <class S, bool PA, bool QA>
+__device__ __forceinline__ void read_frags(const unsigned char* st, int ks, int wp, int wq, int lane, Frags<S>& f) {
+#pragma unroll
+  for (int rb = 0; rb < S::RB; ++rb) f.p[rb] = frag16<S::BP, S::BK / 8, PA>(st, wp * (S::BP / S::WP) + rb * 32, ks, lane);
+#pragma unroll
+  for (int cb = 0; cb < S::CB; ++cb)
+    f.q[cb] = frag16<S::BQ, S::BK / 8, QA>(st + S::P_BYTES, wq * (S::BQ / S::WQ) + cb * 32, ks, lane);
+}
+
+// Instruction order of one step: the next step's fragment reads spread over this
+// step's products, first reads first (left alone, the compiler moves every read
+// down to its use and the wave waits for LDS at each step).
+template <class S, bool PA, bool QA>
+__device__ __forceinline__ void spread_reads() {
+  constexpr int NR = S::RB * (PA ? 2 : 1) + S::CB * (QA ? 2 : 1), NM = S::RB * S::CB;
+  constexpr int PER = (NR + NM - 1) / NM, FULL = NR / PER, REST = NR % PER;  // PER reads before each product
+  static_for<FULL>([](auto) {
+    __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  });
+  if constexpr (REST > 0) __builtin_amdgcn_sched_group_barrier(0x100, REST, 0);
+  if constexpr (NM > FULL) __builtin_amdgcn_sched_group_barrier(0x008, NM - FULL, 0);
+}
+
+// Steps past `left` of a fragment (steps 16 ks + 8 (lane / 32) ..) set to zero.
+__device__ __forceinline__ v8s mask_steps(v8s x, int left) {
+  v4u u = __builtin_bit_cast(v4u, x);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) u[d] = left <= 2 * d ? 0u : left == 2 * d + 1 ? u[d] & 0xffffu : u[d];
+  return __builtin_bit_cast(v8s, u);
+}
+
+// One tile's operands and contraction.
+template <class S>
+struct Tile {
+  Operand P, Q;
+  int64_t steps;
+  int chunks;
+  bool direct;  // every chunk by whole 16-byte units
+  int e, p0, pv, qv;
+  int64_t q0;
+  template <bool PA, bool QA>
+  __device__ __forceinline__ void ready(int64_t n, bool fast) {
+    steps = n;
+    chunks = (int)((n + S::BK - 1) / S::BK);
+    // a ragged edge that splits a unit goes element by element
+    const bool whole_p = PA ? (P.valid == S::BP || P.valid % 8 == 0) : n % 8 == 0;
+    const bool whole_q = QA ? (Q.valid == S::BQ || Q.valid % 8 == 0) : n % 8 == 0;
+    direct = fast && whole_p && whole_q;
+  }
+};
+
+// The loader waves' side of stream_tiles.
+template <class S, bool PA, bool QA, class Load>
+__device__ __forceinline__ void copy_stream(Walk w, bool fast, unsigned char* lds, Load&& load, int loader, int lane) {
+  Tile<S> t;
+  t.chunks = 0;
+  int c = 0, issued = 0;   // next chunk of t; chunks issued so far
+  int edged = -S::NST;     // the last one that was not made of direct copies
+  auto issue = [&] {
+    while (c == t.chunks) {
+      if (w.at >= w.end) return false;
+      load(t, w.at);
+      w.at += w.step;
+      c = 0;
+    }
+    unsigned char* st = lds + issued % S::NST * S::STAGE;
+    const int64_t k0 = (int64_t)c * S::BK;
+    const int left = (int)min((int64_t)S::BK, t.steps - k0);
+    stage_operand<S, S::BP, PA>(t.P, t.direct, fast, k0, left, st, loader, lane);
+    stage_operand<S, S::BQ, QA>(t.Q, t.direct, fast, k0, left, st + S::P_BYTES, loader, lane);
+    if (!t.direct) edged = issued;
+    ++c;
+    ++issued;
+    return true;
+  };
+  for (int i = 0; i < S::NST - 1; ++i) issue();
+  for (int j = 0;; ++j) {
+    // chunk j has landed once at most the copies of the NST - 2 after it are in flight
+    if (issued - 1 - j == S::NST - 2 && edged <= j)
+      wait_vmcnt<(S::NST - 2) * S::COPIES>();
+    else
+      wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // chunk j is in LDS; every wave is done with chunk j - 1
+    asm volatile("" ::: "memory");
+    if (!issue() && j == issued) return;
+  }
+}
+
+// A workgroup's tiles, one after another, as one stream of chunks through NST
+// stages of LDS.  The loader waves copy, up to NST - 1 chunks ahead and into the
+// next tile; the other waves multiply and store.  Only the loaders ever wait for
+// memory, so stores drain behind the next tile's products, and copies cover
+// each other's latency.  One barrier per chunk, before its predecessor's last
+// step of products, whose fragments are in registers by then; one more at the
+// end of the stream.  load(tile, id) describes tile `id`, put(tile, acc, slab)
+// stores one.
+template <class S, typename T, bool PA, bool QA, class Load, class Put>
+__device__ __forceinline__ void stream_tiles(Walk w, bool fast, unsigned char* lds, Load&& load, Put&& put) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= S::NW) {
+    copy_stream<S, PA, QA>(w, fast, lds, load, wave - S::NW, lane);
+    return;
+  }
+  const int wp = wave / S::WQ, wq = wave % S::WQ;
+  unsigned char* slab = lds + S::SLABS + wave * Slab<float>::BYTES;
+  Frags<S> f[2];
+  int g = 0;  // chunk of the stream, in stage g % NST
+  auto join = [&] {
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  join();
+  read_frags<S, PA, QA>(lds, 0, wp, wq, lane, f[0]);
+  v16f acc[S::RB][S::CB];
+  // the products of one chunk; `left` steps of it exist
+  auto chunk = [&](auto tail, int left) {
+    const unsigned char* st = lds + g % S::NST * S::STAGE;
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) {
+      if (ks + 1 < S::KS) {
+        read_frags<S, PA, QA>(st, ks + 1, wp, wq, lane, f[(ks + 1) & 1]);
+      } else {
+        join();
+        ++g;
+        // (past the stream's last chunk these are stale bytes that nothing uses)
+        read_frags<S, PA, QA>(lds + g % S::NST * S::STAGE, 0, wp, wq, lane, f[0]);
+      }
+      Frags<S>& x = f[ks & 1];
+      if constexpr (decltype(tail)::value) {
+        const int n = left - 16 * ks - 8 * (lane >> 5);
+#pragma unroll
+        for (int rb = 0; rb < S::RB; ++rb) x.p[rb] = mask_steps(x.p[rb], n);
+#pragma unroll
+        for (int cb = 0; cb < S::CB; ++cb) x.q[cb] = mask_steps(x.q[cb], n);
+      }
+#pragma unroll
+      for (int rb = 0; rb < S::RB; ++rb)
+#pragma unroll
+        for (int cb = 0; cb < S::CB; ++cb) acc[rb][cb] = mfma16<T>(x.p[rb], x.q[cb], acc[rb][cb]);
+      spread_reads<S, PA, QA>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  for (; w.at < w.end; w.at += w.step) {
+    Tile<S> t;
+    load(t, w.at);
+#pragma unroll
+    for (int rb = 0; rb < S::RB; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[rb][cb][v] = 0.f;
+    const int whole = (int)(t.steps / S::BK), left = (int)(t.steps % S::BK);
+    for (int c = 0; c < whole; ++c) chunk(std::false_type{}, S::BK);
+    if (left) chunk(std::true_type{}, left);
+    put(t, acc, slab);
+  }
+}
+
+// Rows q0 .. of Y from the accumulators, 32 rows of the wave at a time through
+// its part of LDS (a lane holds four consecutive columns of one row).  The
+// lines of a 128-column bf16 tile then leave whole: 25 us less of 181 (64
+// experts, 16384 x 2048 outputs).
+template <class S, typename O>
+__device__ __forceinline__ void put_rows(const GroupedArgs& a, int64_t q0, int qv, int p0, int pv, unsigned char* slab,
+                                         const v16f (&acc)[S::RB][S::CB]) {
+  using W = Slab<O>;
+  constexpr int RP = S::RB < W::COLS / 32 ? S::RB : W::COLS / 32;  // blocks of 32 columns to a slab
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / S::WQ, wq = wave % S::WQ;
 #pragma unroll
-  for (int rb = 0; rb < S::RB; ++rb)
+  for (int cb = 0; cb < S::CB; ++cb) {
+    const int q = wq * (S::BQ / S::WQ) + cb * 32;
 #pragma unroll
-    for (int cb = 0; cb < S::CB; ++cb)
+    for (int r0 = 0; r0 < S::RB; r0 += RP) {
+      const int p = wp * (S::BP / S::WP) + r0 * 32;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[rb][cb][v] = 0.f;
-  const int chunks = (int)((steps + 63) / 64);
-  // an `across` tile at a ragged column edge that splits a 16-byte unit goes element by element
-  const bool p_fast = fast && (!PA || P.valid == S::BP || P.valid % 8 == 0);
-  const bool q_fast = fast && (!QA || Q.valid == S::BQ || Q.valid % 8 == 0);
-  auto issue = [&](int c) {
-    unsigned char* st = lds + (c & 1) * S::STAGE;
-    const int64_t k0 = (int64_t)c * 64;
-    const int left = (int)min((int64_t)64, steps - k0);
-    if constexpr (PA) {
-      if (p_fast && left == 64)
-        copy_across<S::BP, S::NW>(P.base, P.ld_bytes, k0, P.r0, P.valid, st, wave, lane);
-      else
-        edge_across<S::BP, S::THREADS>(P.base, P.ld_bytes, k0, left, P.r0, P.valid, fast, st);
-    } else {
-      if (p_fast && left == 64)
-        copy_along<S::BP, S::NW>(P.base, P.ld_bytes, P.r0, P.valid, k0 * 2, st, wave, lane);
-      else
-        edge_along<S::BP, S::THREADS, 2>(P.base, P.ld_bytes, P.r0, P.valid, k0 * 2, left, fast, st);
-    }
-    st += S::P_BYTES;
-    if constexpr (QA) {
-      if (q_fast && left == 64)
-        copy_across<S::BQ, S::NW>(Q.base, Q.ld_bytes, k0, Q.r0, Q.valid, st, wave, lane);
-      else
-        edge_across<S::BQ, S::THREADS>(Q.base, Q.ld_bytes, k0, left, Q.r0, Q.valid, fast, st);
-    } else {
-      if (q_fast && left == 64)
-        copy_along<S::BQ, S::NW>(Q.base, Q.ld_bytes, Q.r0, Q.valid, k0 * 2, st, wave, lane);
-      else
-        edge_along<S::BQ, S::THREADS, 2>(Q.base, Q.ld_bytes, Q.r0, Q.valid, k0 * 2, left, fast, st);
-    }
-  };
-  if (chunks > 0) issue(0);
-  for (int c = 0; c < chunks; ++c) {
-    stage_barrier();  // chunk c is in LDS; every wave is done with chunk c - 1
-    if (c + 1 < chunks) issue(c + 1);
-    const unsigned char* st = lds + (c & 1) * S::STAGE;
+      for (int rb = 0; rb < RP; ++rb)
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      v8s p[S::RB], q[S::CB];
-#pragma unroll
-      for (int rb = 0; rb < S::RB; ++rb) p[rb] = frag16<S::BP, PA>(st, wp * (S::BP / S::WP) + rb * 32, ks, lane);
-#pragma unroll
-      for (int cb = 0; cb < S::CB; ++cb) q[cb] = frag16<S::BQ, QA>(st + S::P_BYTES, wq * (S::BQ / S::WQ) + cb * 32, ks, lane);
-#pragma unroll
-      for (int rb = 0; rb < S::RB; ++rb)
-#pragma unroll
-        for (int cb = 0; cb < S::CB; ++cb) acc[rb][cb] = mfma16<T>(p[rb], q[cb], acc[rb][cb]);
+        for (int u = 0; u < 4; ++u) {
+          const v16f& x = acc[r0 + rb][cb];
+          const float v[4] = {x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]};
+          W::put4(slab, lane & 31, rb * 32 + 8 * u + 4 * (lane >> 5), v);
+        }
+      W::fence();
+      W::store(slab, reinterpret_cast<O*>(a.y) + (q0 + q) * a.ldy + p0 + p, a.ldy, qv - q, min(pv - p, RP * 32), a.vec_y,
+               false, lane);
+      W::fence();
     }
   }
 }
 
-// Rows q0 .. of Y (leading dimension ldy) from the accumulators, or zeros.
-template <class S, typename T>
-__device__ __forceinline__ void put_tile(const GroupedArgs& a, char* y, int64_t q0, int qv, int p0, int pv,
-                                         const v16f (&acc)[S::RB][S::CB]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// A weight's gradient from the accumulators: P's rows are its rows, Q's its
+// columns, so 32 lanes store 32 consecutive columns (a whole 128-byte line of
+// float32) of one row.
+template <class S, typename O>
+__device__ __forceinline__ void put_weight(const GroupedArgs& a, O* w, int p0, int pv, int q0, int qv,
+                                           const v16f (&acc)[S::RB][S::CB]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / S::WQ, wq = wave % S::WQ;
-#pragma unroll
-  for (int cb = 0; cb < S::CB; ++cb) {
-    const int qr = wq * (S::BQ / S::WQ) + cb * 32 + (lane & 31);
-    if (qr >= qv) continue;
-    const int64_t row = (q0 + qr) * a.ldy;
+  if (pv == S::BP && qv == S::BQ && !a.accumulate) {
+    // a whole tile: scalar row addresses, one 32-bit lane offset (with the checks of the general
+    // form below the stores took longer than the products)
+    O* base = w + (int64_t)(p0 + wp * (S::BP / S::WP)) * a.ldy + q0 + wq * (S::BQ / S::WQ);
+    const uint32_t off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)a.ldy + (uint32_t)(lane & 31);
 #pragma unroll
     for (int rb = 0; rb < S::RB; ++rb)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int pr = wp * (S::BP / S::WP) + rb * 32 + 8 * u + 4 * (lane >> 5);
-        if (pr >= pv) continue;
-        const float v[4] = {acc[rb][cb][4 * u], acc[rb][cb][4 * u + 1], acc[rb][cb][4 * u + 2], acc[rb][cb][4 * u + 3]};
-        if (a.y_f32)
-          put4(reinterpret_cast<float*>(y) + row + p0 + pr, v, pv - pr, a.vec_y, a.accumulate);
-        else
-          put4(reinterpret_cast<T*>(y) + row + p0 + pr, v, pv - pr, a.vec_y, a.accumulate);
+      for (int v = 0; v < 16; ++v) {
+        O* row = base + (int64_t)(rb * 32 + 8 * (v >> 2) + (v & 3)) * a.ldy;
+#pragma unroll
+        for (int cb = 0; cb < S::CB; ++cb) store_once(narrow<O>(acc[rb][cb][v]), row + off + cb * 32);
       }
+    return;
   }
+#pragma unroll
+  for (int rb = 0; rb < S::RB; ++rb)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int pr = wp * (S::BP / S::WP) + rb * 32 + f32_row(lane, v);
+      if (pr >= pv) continue;
+      O* row = w + (int64_t)(p0 + pr) * a.ldy + q0;
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) {
+        const int qc = wq * (S::BQ / S::WQ) + cb * 32 + (lane & 31);
+        if (qc >= qv) continue;
+        const float x = a.accumulate ? acc[rb][cb][v] + widen(row[qc]) : acc[rb][cb][v];
+        row[qc] = narrow<O>(x);
+      }
+    }
 }
 
 template <class S, typename T, bool TRANSPOSE>
-__global__ __launch_bounds__(S::THREADS) void grouped_tile_kernel(const GroupedArgs a) {
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_kernel(const GroupedArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
   const int outs = TRANSPOSE ? a.k : a.n, steps = TRANSPOSE ? a.n : a.k;
-  const int across = (outs + S::BP - 1) / S::BP;
-  int seg, local;
-  int64_t begin, end;
-  if (!find_tile<S::BQ>(a, xcd_remap(blockIdx.x, gridDim.x), across, seg, begin, end, local)) return;
-  // an expert's row tiles follow one another under one panel of its weight
-  const int down = (int)((end - begin + S::BQ - 1) / S::BQ);
-  const int p0 = local / down * S::BP;
-  const int64_t q0 = begin + (int64_t)(local % down) * S::BQ;
-  const int pv = min(S::BP, outs - p0), qv = (int)min((int64_t)S::BQ, end - q0);
-  const bool expert = seg >= 1 && seg <= a.experts;
-  const unsigned char* w = reinterpret_cast<const unsigned char*>(a.w) + (expert ? seg - 1 : 0) * a.w_stride * 2;
-  const Operand P{w, a.ldw * 2, p0, pv};
-  const Operand Q{reinterpret_cast<const unsigned char*>(a.x), a.ldx * 2, q0, qv};
-  v16f acc[S::RB][S::CB];
-  grouped_tile<S, T, TRANSPOSE, false>(P, Q, expert ? steps : 0, a.fast, lds, acc);
-  put_tile<S, T>(a, reinterpret_cast<char*>(a.y), q0, qv, p0, pv, acc);
+  RowTiles<S::BQ> tiles;
+  tiles.count(a, (outs + S::BP - 1) / S::BP);
+  auto load = [&](Tile<S>& t, int id) {
+    int64_t begin, end;
+    int local;
+    tiles.find(a, id, t.e, begin, end, local);
+    // an expert's row tiles follow one another under one panel of its weight
+    // (offsets that decrease break the count: the bounds keep even those tiles inside the matrices)
+    const int down = max((int)((end - begin + S::BQ - 1) / S::BQ), 1);
+    t.p0 = min(max(local / down, 0), tiles.across - 1) * S::BP;
+    t.q0 = begin + (int64_t)max(local % down, 0) * S::BQ;
+    t.pv = min(S::BP, outs - t.p0);
+    t.qv = (int)min((int64_t)S::BQ, end - t.q0);
+    t.P = Operand{reinterpret_cast<const unsigned char*>(a.w) + t.e * a.w_stride * 2, a.ldw * 2, t.p0, t.pv};
+    t.Q = Operand{reinterpret_cast<const unsigned char*>(a.x), a.ldx * 2, t.q0, t.qv};
+    t.template ready<TRANSPOSE, false>(t.qv > 0 ? steps : 0, a.fast);
+  };
+  auto put = [&](const Tile<S>& t, const v16f(&acc)[S::RB][S::CB], unsigned char* slab) {
+    if (a.y_f32)
+      put_rows<S, float>(a, t.q0, t.qv, t.p0, t.pv, slab, acc);
+    else
+      put_rows<S, T>(a, t.q0, t.qv, t.p0, t.pv, slab, acc);
+  };
+  stream_tiles<S, T, TRANSPOSE, false>(Walk(tiles.total), a.fast, lds, load, put);
+  // rows of no expert: before the first and after the last offset
+  const int64_t first = offset_at(a, 0), last = max(offset_at(a, a.experts), first);
+  const int es = a.y_f32 ? 4 : 2;
+  for (int64_t r = blockIdx.x; r < first + a.rows - last; r += gridDim.x) {
+    char* row = reinterpret_cast<char*>(a.y) + (r < first ? r : r - first + last) * a.ldy * es;
+    for (int c = threadIdx.x; c < outs; c += S::THREADS) {
+      if (a.y_f32)
+        reinterpret_cast<float*>(row)[c] = 0.f;
+      else
+        reinterpret_cast<uint16_t*>(row)[c] = 0;
+    }
+  }
 }
 
 template <class S, typename T>
-__global__ __launch_bounds__(S::THREADS) void grouped_weight_kernel(const GroupedArgs a) {
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_kernel(const GroupedArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
-  const int tp = (a.k + S::BP - 1) / S::BP, tq = (a.n + S::BQ - 1) / S::BQ;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int e = (int)(id / (tp * tq)), local = (int)(id % (tp * tq));
-  int64_t begin, end;
-  segment(a, e + 1, begin, end);
-  const int p0 = local % tp * S::BP, q0 = local / tp * S::BQ;
-  const int pv = min(S::BP, a.k - p0), qv = min(S::BQ, a.n - q0);
-  const Operand P{reinterpret_cast<const unsigned char*>(a.w) + begin * a.ldw * 2, a.ldw * 2, p0, pv};
-  const Operand Q{reinterpret_cast<const unsigned char*>(a.x) + begin * a.ldx * 2, a.ldx * 2, q0, qv};
-  v16f acc[S::RB][S::CB];
-  grouped_tile<S, T, true, true>(P, Q, end - begin, a.fast, lds, acc);
-  char* y = reinterpret_cast<char*>(a.y) + e * a.y_stride * (a.y_f32 ? 4 : 2);
-  put_tile<S, T>(a, y, q0, qv, p0, pv, acc);
+  const int tp = (a.n + S::BP - 1) / S::BP, tq = (a.k + S::BQ - 1) / S::BQ;
+  auto load = [&](Tile<S>& t, int id) {
+    t.e = id / (tp * tq);
+    const int local = id % (tp * tq);
+    int64_t begin, end;
+    expert_rows(a, t.e, begin, end);
+    t.p0 = local / tq * S::BP;
+    t.q0 = local % tq * S::BQ;
+    t.pv = min(S::BP, a.n - t.p0);
+    t.qv = min(S::BQ, a.k - (int)t.q0);
+    t.P = Operand{reinterpret_cast<const unsigned char*>(a.x) + begin * a.ldx * 2, a.ldx * 2, t.p0, t.pv};
+    t.Q = Operand{reinterpret_cast<const unsigned char*>(a.w) + begin * a.ldw * 2, a.ldw * 2, t.q0, t.qv};
+    t.template ready<true, true>(end - begin, a.fast);
+  };
+  auto put = [&](const Tile<S>& t, const v16f(&acc)[S::RB][S::CB], unsigned char*) {
+    if (a.y_f32)
+      put_weight<S>(a, reinterpret_cast<float*>(a.y) + t.e * a.y_stride, t.p0, t.pv, (int)t.q0, t.qv, acc);
+    else
+      put_weight<S>(a, reinterpret_cast<T*>(a.y) + t.e * a.y_stride, t.p0, t.pv, (int)t.q0, t.qv, acc);
+  };
+  stream_tiles<S, T, true, true>(Walk(a.experts * tp * tq), a.fast, lds, load, put);
 }
 
 // ------------------------------------------------------------ launchers
 namespace {
 
-using Tile128 = GroupedShape<128, 128, 2, 2>;
+#ifndef RWS
+#define RWS 256, 128, 2, 2, 64, 3, 1
+#endif
+#ifndef WSH
+#define WSH 256, 128, 2, 2, 64, 3, 1
+#endif
+using RowsWide = GroupedShape<RWS>;
+using RowsNarrow = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
+using RowsFew = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
+using Weights = GroupedShape<WSH>;
+
+// Workgroups of a launch over at most `tiles` tiles: what the CUs hold at a
+// time, a multiple of the XCDs.
+unsigned persistent_blocks(int64_t tiles, int per_cu) {
+  const int64_t most = 256 * per_cu;
+  return (unsigned)(tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most);
+}
 
 template <class K>
 hipError_t raise_lds(K kernel, int bytes, bool& raised) {
@@ -271,9 +521,9 @@ hipError_t go_rows(const GroupedArgs& a, hipStream_t s) {
   auto kernel = grouped_tile_kernel<S, T, TRANSPOSE>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t outs = TRANSPOSE ? a.k : a.n;
-  const int64_t segments = a.experts + 2 < a.rows ? a.experts + 2 : a.rows;
-  const int64_t tiles = (a.rows / S::BQ + segments) * ((outs + S::BP - 1) / S::BP);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(S::THREADS), S::LDS, s, a);
+  const int64_t groups = a.experts < a.rows ? a.experts : a.rows;
+  const int64_t tiles = (a.rows / S::BQ + groups) * ((outs + S::BP - 1) / S::BP);  // at most
+  hipLaunchKernelGGL(kernel, dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
 }
 
@@ -282,20 +532,28 @@ hipError_t go_weights(const GroupedArgs& a, hipStream_t s) {
   static bool raised = false;
   auto kernel = grouped_weight_kernel<S, T>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
-  const int64_t tiles = (int64_t)a.experts * ((a.k + S::BP - 1) / S::BP) * ((a.n + S::BQ - 1) / S::BQ);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(S::THREADS), S::LDS, s, a);
+  const int64_t tiles = (int64_t)a.experts * ((a.n + S::BP - 1) / S::BP) * ((a.k + S::BQ - 1) / S::BQ);
+  hipLaunchKernelGGL(kernel, dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
+}
+
+template <typename T, bool TRANSPOSE>
+hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
+  const int outs = TRANSPOSE ? a.k : a.n;
+  if (a.rows <= 32 * (int64_t)a.experts) return go_rows<RowsFew, T, TRANSPOSE>(a, s);
+  if (outs > 128) return go_rows<RowsWide, T, TRANSPOSE>(a, s);
+  return go_rows<RowsNarrow, T, TRANSPOSE>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs& a, mr_dtype dt, bool transpose, hipStream_t s) {
-  if (dt == MR_F16) return transpose ? go_rows<Tile128, _Float16, true>(a, s) : go_rows<Tile128, _Float16, false>(a, s);
-  return transpose ? go_rows<Tile128, bf16_t, true>(a, s) : go_rows<Tile128, bf16_t, false>(a, s);
+  if (dt == MR_F16) return transpose ? pick_rows<_Float16, true>(a, s) : pick_rows<_Float16, false>(a, s);
+  return transpose ? pick_rows<bf16_t, true>(a, s) : pick_rows<bf16_t, false>(a, s);
 }
 
 hipError_t launch_grouped_weight_grad(const GroupedArgs& a, mr_dtype dt, hipStream_t s) {
-  return dt == MR_F16 ? go_weights<Tile128, _Float16>(a, s) : go_weights<Tile128, bf16_t>(a, s);
+  return dt == MR_F16 ? go_weights<Weights, _Float16>(a, s) : go_weights<Weights, bf16_t>(a, s);
 }
 
 }  // namespace mr

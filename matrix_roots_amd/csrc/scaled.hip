@@ -147,11 +147,11 @@ __global__ __launch_bounds__(S::THREADS) void scaled_tile_kernel(const ScaledArg
     const int64_t k0 = (int64_t)c * kChunkBytes;
     const int left = a.k - (int)k0;
     if (a.fast && left >= kChunkBytes) {
-      copy_along<S::BP, S::NW>(a.p, a.ldp, p0, pv, k0, st, wave, lane);
-      copy_along<S::BQ, S::NW>(a.q, a.ldq, q0, qv, k0, st + S::P_BYTES, wave, lane);
+      copy_along<S::BP, S::NW, 8>(a.p, a.ldp, p0, pv, k0, 8, st, wave, lane);
+      copy_along<S::BQ, S::NW, 8>(a.q, a.ldq, q0, qv, k0, 8, st + S::P_BYTES, wave, lane);
     } else {
-      edge_along<S::BP, S::THREADS, 1>(a.p, a.ldp, p0, pv, k0, left, a.fast, st);
-      edge_along<S::BQ, S::THREADS, 1>(a.q, a.ldq, q0, qv, k0, left, a.fast, st + S::P_BYTES);
+      edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, p0, pv, k0, left, a.fast, st, threadIdx.x);
+      edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, q0, qv, k0, left, a.fast, st + S::P_BYTES, threadIdx.x);
     }
     if (PVEC) {
       float* s = reinterpret_cast<float*>(st + S::P_BYTES + S::Q_BYTES);

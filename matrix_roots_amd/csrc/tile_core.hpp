@@ -1,13 +1,13 @@
-// LDS tiles of the linear-layer products: operand chunks of 128 bytes of the
-// contraction per row, copied straight from global memory (16 bytes per lane)
+// LDS tiles of the linear-layer products: operand chunks of 64 or 128 bytes of
+// the contraction per row, copied straight from global memory (16 bytes per lane)
 // where whole units exist, element by element at the edges.
 //
 // Two forms of an operand tile with R rows of the product:
-//  * along:  the contraction is contiguous in memory.  R LDS rows of 128 bytes
-//    (8 units of 16); unit u of row r lies in slot u ^ ((r / 2) % 8), so the 16
-//    rows one read cycle touches lie in 16 different bank groups.
+//  * along:  the contraction is contiguous in memory.  R LDS rows of UPR units of
+//    16 bytes; unit u of row r lies in slot dl_slot(r, u, UPR), so the 16 rows
+//    one read cycle touches lie in 16 different bank groups.
 //  * across: the product's rows are contiguous in memory (the transposed
-//    operand; 16-bit types).  64 LDS rows (steps of the contraction) of 2 R
+//    operand; 16-bit types).  LDS rows are steps of the contraction, of 2 R
 //    bytes; unit u of row r lies in slot u ^ across_swap(r), so that the four
 //    rows a transposing read takes at once lie in different banks.
 #pragma once
@@ -25,33 +25,35 @@ __device__ __forceinline__ int across_swap(int row) {
   return UPR >= 16 ? 4 * (row & 3) : 2 * (row & 3);
 }
 
-// A chunk of an `along` tile by direct copies: rows row0 .. row0 + R - 1 of P
-// (row pointers at base + row * ld bytes), the 128 bytes from byte k0.  Rows
-// past `valid` re-read the last one: they only feed outputs that are never
-// stored.
-template <int R, int NW>
+// A chunk of an `along` tile by direct copies of NW waves: rows row0 .. row0 + R
+// - 1 of P (row pointers at base + row * ld bytes), the 16 UPR bytes from byte
+// k0.  Rows past `valid` re-read the last one: they only feed outputs that are
+// never stored.  Units past the first `units` re-read the last one: the reader
+// masks those steps.
+template <int R, int NW, int UPR>
 __device__ __forceinline__ void copy_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
-                                           unsigned char* stage, int wave, int lane) {
-  constexpr int N = R * 8 / 64 / NW;
-  static_assert(N * 64 * NW == R * 8, "copies cover the chunk");
+                                           int units, unsigned char* stage, int wave, int lane) {
+  constexpr int N = R * UPR / 64 / NW;
+  static_assert(N * 64 * NW == R * UPR, "copies cover the chunk");
   const char* p = wave_uniform(base + row0 * ld_bytes + k0);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const int u0 = (j * NW + wave) * 64;
-    const int u = u0 + lane, row = u >> 3;
-    uint32_t off = (uint32_t)min(row, valid - 1) * (uint32_t)ld_bytes + (uint32_t)(dl_slot(row, u & 7, 8) * 16);
+    const int u = u0 + lane, row = u / UPR;
+    uint32_t off = (uint32_t)min(row, valid - 1) * (uint32_t)ld_bytes + (uint32_t)(min(dl_slot(row, u % UPR, UPR), units - 1) * 16);
     asm volatile("" : "+v"(off));  // opaque per copy: the offset stays a 32-bit lane value
     __builtin_amdgcn_global_load_lds((global_void_ptr)(p + off), (lds_void_ptr)(stage + u0 * 16), 16, 0, 0);
   }
 }
 
-// A chunk of an `across` tile: contraction rows k0 .. k0 + 63, the R columns
-// from col0 (16-bit elements), all inside the matrix.
-template <int R, int NW>
-__device__ __forceinline__ void copy_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int64_t col0, int valid,
-                                            unsigned char* stage, int wave, int lane) {
-  constexpr int UPR = R / 8, N = 64 * UPR / 64 / NW;
-  static_assert(N * NW == UPR, "copies cover the chunk");
+// A chunk of an `across` tile: contraction rows k0 .. k0 + BK - 1, the R columns
+// from col0 (16-bit elements); steps past `left` re-read the last one, columns
+// past `valid` (a multiple of 8 there) the last unit.
+template <int R, int NW, int BK>
+__device__ __forceinline__ void copy_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int left, int64_t col0,
+                                            int valid, unsigned char* stage, int wave, int lane) {
+  constexpr int UPR = R / 8, N = BK * UPR / 64 / NW;
+  static_assert(N * NW * 64 == BK * UPR, "copies cover the chunk");
   const char* p = wave_uniform(base + k0 * ld_bytes + col0 * 2);
   const int units = (valid + 7) >> 3;
 #pragma unroll
@@ -59,7 +61,7 @@ __device__ __forceinline__ void copy_across(const unsigned char* base, int64_t l
     const int u0 = (j * NW + wave) * 64;
     const int u = u0 + lane, row = u / UPR;
     const int unit = (u % UPR) ^ across_swap<R>(row);
-    uint32_t off = (uint32_t)row * (uint32_t)ld_bytes + (uint32_t)(min(unit, units - 1) * 16);
+    uint32_t off = (uint32_t)min(row, left - 1) * (uint32_t)ld_bytes + (uint32_t)(min(unit, units - 1) * 16);
     asm volatile("" : "+v"(off));
     __builtin_amdgcn_global_load_lds((global_void_ptr)(p + off), (lds_void_ptr)(stage + u0 * 16), 16, 0, 0);
   }
@@ -79,24 +81,25 @@ __device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n, bool ali
   return r;
 }
 
-// The same chunks with every element checked: rows past `valid` and contraction
+// The same chunks by the THREADS threads from `thread` on with every element
+// checked: rows past `valid` and contraction
 // steps past k_left are zeros, so that nothing that lies there (not even a NaN)
 // reaches the sums.
-template <int R, int THREADS, int ES>
+template <int R, int THREADS, int ES, int UPR>
 __device__ __forceinline__ void edge_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
-                                           int k_left, bool aligned, unsigned char* stage) {
-  for (int u = threadIdx.x; u < R * 8; u += THREADS) {
-    const int row = u >> 3, unit = u & 7;
+                                           int k_left, bool aligned, unsigned char* stage, int thread) {
+  for (int u = thread; u < R * UPR; u += THREADS) {
+    const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
     if (row < valid) v = edge_unit<ES>(base + (row0 + row) * ld_bytes + k0 + unit * 16, k_left - unit * (16 / ES), aligned);
-    *reinterpret_cast<v4u*>(stage + (row * 8 + dl_slot(row, unit, 8)) * 16) = v;
+    *reinterpret_cast<v4u*>(stage + (row * UPR + dl_slot(row, unit, UPR)) * 16) = v;
   }
 }
-template <int R, int THREADS>
+template <int R, int THREADS, int BK>
 __device__ __forceinline__ void edge_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int k_left, int64_t col0,
-                                            int valid, bool aligned, unsigned char* stage) {
+                                            int valid, bool aligned, unsigned char* stage, int thread) {
   constexpr int UPR = R / 8;
-  for (int u = threadIdx.x; u < 64 * UPR; u += THREADS) {
+  for (int u = thread; u < BK * UPR; u += THREADS) {
     const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
     if (row < k_left) v = edge_unit<2>(base + (k0 + row) * ld_bytes + (col0 + unit * 8) * 2, valid - unit * 8, aligned);
@@ -141,6 +144,54 @@ __device__ __forceinline__ void put4_as(void* c, int64_t at, const float (&v)[4]
   else
     put4(reinterpret_cast<bf16_t*>(c) + at, v, left, vec, accumulate);
 }
+
+// 32 rows of outputs of one wave through LDS, so that they leave in 16-byte
+// units: 128 bytes of O to a row, unit u of row r in slot u ^ (r % 8).  The
+// wave's LDS instructions run in order, so only the compiler has to keep them so.
+template <typename O>
+struct Slab {
+  static constexpr int COLS = 128 / (int)sizeof(O), BYTES = 32 * 128, EU = 16 / (int)sizeof(O);
+  static __device__ __forceinline__ void put4(unsigned char* slab, int row, int col, const float (&v)[4]) {
+    O t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = narrow<O>(v[i]);
+    unsigned char* p = slab + row * 128 + ((col / EU) ^ (row & 7)) * 16 + col % EU * (int)sizeof(O);
+    if constexpr (sizeof(O) == 4) {
+      v4u u;
+      __builtin_memcpy(&u, t, 16);
+      *reinterpret_cast<v4u*>(p) = u;
+    } else {
+      v2u u;
+      __builtin_memcpy(&u, t, 8);
+      *reinterpret_cast<v2u*>(p) = u;
+    }
+  }
+  static __device__ __forceinline__ void fence() {
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // rows_left x cols_left of the slab exist in c
+  static __device__ __forceinline__ void store(const unsigned char* slab, O* c, int64_t ldc, int rows_left, int cols_left,
+                                               bool vec, bool accumulate, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 8 * j + (lane >> 3), unit = lane & 7, col = unit * EU;
+      if (row >= rows_left || col >= cols_left) continue;
+      const v4u x = *reinterpret_cast<const v4u*>(slab + row * 128 + (unit ^ (row & 7)) * 16);
+      O* p = c + row * ldc + col;
+      if (vec && !accumulate && col + EU <= cols_left) {
+        *reinterpret_cast<v4u*>(p) = x;
+        continue;
+      }
+      O t[EU];
+      __builtin_memcpy(t, &x, 16);
+#pragma unroll
+      for (int i = 0; i < EU; ++i)
+        if (col + i < cols_left) p[i] = accumulate ? narrow<O>(widen(t[i]) + widen(p[i])) : t[i];
+    }
+  }
+};
 
 // This wave's copies and LDS stores are done, and so are every other wave's.
 __device__ __forceinline__ void stage_barrier() {
