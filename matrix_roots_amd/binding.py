@@ -130,7 +130,7 @@ class ScaledMatmulProblem(ctypes.Structure):
                 ("ldb", ctypes.c_int64), ("SB", ctypes.c_void_p), ("ldsb", ctypes.c_int64), ("C", ctypes.c_void_p),
                 ("ldc", ctypes.c_int64), ("a_dtype", ctypes.c_int32), ("b_dtype", ctypes.c_int32),
                 ("c_dtype", ctypes.c_int32), ("a_block", ctypes.c_int32), ("b_block", ctypes.c_int32),
-                ("accumulate", ctypes.c_int32)]
+                ("accumulate", ctypes.c_int32), ("padded", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class GroupedProblem(ctypes.Structure):

@@ -46,8 +46,9 @@ __device__ __forceinline__ v16f mfma16<bf16_t>(v8s p, v8s q, v16f c) {
 template <int R, int UPK, bool ACROSS>
 __device__ __forceinline__ v8s frag16(const unsigned char* st, int row, int ks, int lane) {
   if constexpr (!ACROSS) {
-    const int r = row + (lane & 31);
-    return *reinterpret_cast<const v8s*>(st + (r * UPK + dl_slot(r, 2 * ks + (lane >> 5), UPK)) * 16);
+    // (row is a multiple of 32: the slot depends on the lane alone)
+    const int r = lane & 31;
+    return *reinterpret_cast<const v8s*>(st + row * UPK * 16 + (r * UPK + dl_slot(r, 2 * ks + (lane >> 5), UPK)) * 16);
   } else {
     // 16 lanes read four steps x 16 columns (lane i: step i / 4, columns 4 (i % 4) ..)
     // and each gets the four steps of column i
@@ -118,24 +119,10 @@ struct RowTiles {
   }
 };
 
-// Tiles of a persistent workgroup: tile k of slot b / 8 on XCD b % 8, where
-// every XCD owns one run of `total` / 8 tiles and walks it in order, so that
-// the tiles in flight on an XCD are neighbours and share operands in its L2.
-struct Walk {
-  int at, step, end;
-  __device__ __forceinline__ Walk(int total) {
-    const int x = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
-    end = (int)((int64_t)total * (x + 1) / kNumXcd);
-    at = (int)((int64_t)total * x / kNumXcd) + blockIdx.x / kNumXcd;
-    step = slots;
-  }
-};
-
 }  // namespace
 
 // WP x WQ waves multiply, kLoaders waves copy.  NST stages of BK steps in LDS;
 // BPC workgroups to a CU.
-constexpr int kLoaders = 4;
 template <int BP_, int BQ_, int WP_, int WQ_, int BK_, int NST_, int BPC_>
 struct GroupedShape {
   static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NW = WP * WQ, BK = BK_, NST = NST_, BPC = BPC_;
@@ -144,7 +131,7 @@ struct GroupedShape {
   static constexpr int P_BYTES = BP * BK * 2, STAGE = (BP + BQ) * BK * 2;
   static constexpr int COPIES = STAGE / 1024 / kLoaders;  // direct copies per loader wave and chunk
   static constexpr int SLABS = NST * STAGE;               // where the waves' output slabs start
-  static constexpr int LDS = SLABS + NW * Slab<float>::BYTES;
+  static constexpr int LDS = SLABS + NW * Slab<float, 32>::BYTES;
   static constexpr int WAVES_PER_SIMD = (BPC * (NW + kLoaders) + 3) / 4;
   static_assert(KS % 2 == 0 && BPC * LDS <= 160 * 1024, "fragments alternate; the stages fit");
 };
@@ -235,38 +222,22 @@ template <class S, bool PA, bool QA, class Load>
 __device__ __forceinline__ void copy_stream(Walk w, bool fast, unsigned char* lds, Load&& load, int loader, int lane) {
   Tile<S> t;
   t.chunks = 0;
-  int c = 0, issued = 0;   // next chunk of t; chunks issued so far
-  int edged = -S::NST;     // the last one that was not made of direct copies
-  auto issue = [&] {
+  int c = 0;  // next chunk of t
+  copy_chunks<S::NST, S::COPIES>([&](int j) {
     while (c == t.chunks) {
-      if (w.at >= w.end) return false;
+      if (w.at >= w.end) return -1;
       load(t, w.at);
       w.at += w.step;
       c = 0;
     }
-    unsigned char* st = lds + issued % S::NST * S::STAGE;
+    unsigned char* st = lds + j % S::NST * S::STAGE;
     const int64_t k0 = (int64_t)c * S::BK;
     const int left = (int)min((int64_t)S::BK, t.steps - k0);
     stage_operand<S, S::BP, PA>(t.P, t.direct, fast, k0, left, st, loader, lane);
     stage_operand<S, S::BQ, QA>(t.Q, t.direct, fast, k0, left, st + S::P_BYTES, loader, lane);
-    if (!t.direct) edged = issued;
     ++c;
-    ++issued;
-    return true;
-  };
-  for (int i = 0; i < S::NST - 1; ++i) issue();
-  for (int j = 0;; ++j) {
-    // chunk j has landed once at most the copies of the NST - 2 after it are in flight
-    if (issued - 1 - j == S::NST - 2 && edged <= j)
-      wait_vmcnt<(S::NST - 2) * S::COPIES>();
-    else
-      wait_vmcnt<0>();
-    wait_lgkmcnt0();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // chunk j is in LDS; every wave is done with chunk j - 1
-    asm volatile("" ::: "memory");
-    if (!issue() && j == issued) return;
-  }
+    return t.direct ? 1 : 0;
+  });
 }
 
 // A workgroup's tiles, one after another, as one stream of chunks through NST
@@ -286,16 +257,10 @@ __device__ __forceinline__ void stream_tiles(Walk w, bool fast, unsigned char* l
     return;
   }
   const int wp = wave / S::WQ, wq = wave % S::WQ;
-  unsigned char* slab = lds + S::SLABS + wave * Slab<float>::BYTES;
+  unsigned char* slab = lds + S::SLABS + wave * Slab<float, 32>::BYTES;
   Frags<S> f[2];
   int g = 0;  // chunk of the stream, in stage g % NST
-  auto join = [&] {
-    wait_lgkmcnt0();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  join();
+  join_chunk();
   read_frags<S, PA, QA>(lds, 0, wp, wq, lane, f[0]);
   v16f acc[S::RB][S::CB];
   // the products of one chunk; `left` steps of it exist
@@ -306,7 +271,7 @@ __device__ __forceinline__ void stream_tiles(Walk w, bool fast, unsigned char* l
       if (ks + 1 < S::KS) {
         read_frags<S, PA, QA>(st, ks + 1, wp, wq, lane, f[(ks + 1) & 1]);
       } else {
-        join();
+        join_chunk();
         ++g;
         // (past the stream's last chunk these are stale bytes that nothing uses)
         read_frags<S, PA, QA>(lds + g % S::NST * S::STAGE, 0, wp, wq, lane, f[0]);
@@ -350,7 +315,7 @@ __device__ __forceinline__ void stream_tiles(Walk w, bool fast, unsigned char* l
 template <class S, typename O>
 __device__ __forceinline__ void put_rows(const GroupedArgs& a, int64_t q0, int qv, int p0, int pv, unsigned char* slab,
                                          const v16f (&acc)[S::RB][S::CB]) {
-  using W = Slab<O>;
+  using W = Slab<O, 32>;
   constexpr int RP = S::RB < W::COLS / 32 ? S::RB : W::COLS / 32;  // blocks of 32 columns to a slab
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -499,13 +464,6 @@ using RowsWide = GroupedShape<RWS>;
 using RowsNarrow = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
 using RowsFew = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
 using Weights = GroupedShape<WSH>;
-
-// Workgroups of a launch over at most `tiles` tiles: what the CUs hold at a
-// time, a multiple of the XCDs.
-unsigned persistent_blocks(int64_t tiles, int per_cu) {
-  const int64_t most = 256 * per_cu;
-  return (unsigned)(tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most);
-}
 
 template <class K>
 hipError_t raise_lds(K kernel, int bytes, bool& raised) {

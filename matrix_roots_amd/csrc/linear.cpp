@@ -277,11 +277,11 @@ mr_status block_scaled_matmul(const mr_scaled_matmul_problem* p, void* ws, size_
   a.c = p->C, a.ldc = p->ldc, a.c_type = p->c_dtype;
   a.partial = static_cast<float*>(need ? ws : nullptr);
   a.m = p->m, a.n = (int32_t)p->n, a.k = (int32_t)p->k;
-  a.p_vector = !b_square, a.q_shift = a_square ? 7 : 0;
-  a.fast = units16(p->A, p->lda, 1) && units16(p->B, p->ldb, 1);
+  a.p_vector = !b_square, a.p_shift = b_square ? 7 : 0, a.q_shift = a_square ? 7 : 0;
+  a.fast = units16(p->A, p->lda, 1) && units16(p->B, p->ldb, 1) && (p->k % 16 == 0 || p->padded);
   a.q_e5m2 = p->a_dtype == MR_E5M2;
   a.accumulate = p->accumulate != 0;
-  a.vec_c = aligned(p->C, 4 * cs) && p->ldc % 4 == 0;
+  a.vec_c = units16(p->C, p->ldc, cs);
   a.splits = plan.splits;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   MR_TRY(traced(kTrScaledMatmul, true, s, [&] { return launch_scaled(a, plan, s); }, "block-scaled product launch"));

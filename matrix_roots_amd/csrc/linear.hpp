@@ -68,6 +68,7 @@ struct ScaledArgs {
   int64_t m;
   int32_t n, k;
   int32_t p_vector;        // P's scales: one per row (else per 128 rows)
+  int32_t p_shift;         // P's scales: row >> p_shift (0: one per row, 7: per 128 rows)
   int32_t q_shift;         // Q's scales: row >> q_shift (0: one per row, 7: per 128 rows)
   int32_t fast;            // rows of both operands in 16-byte units
   int32_t q_e5m2;
@@ -77,7 +78,7 @@ struct ScaledArgs {
   int32_t splits;
 };
 struct ScaledPlan {
-  int kind;    // 0: few rows (no LDS tile), 1: 128 x 128 tiles, 2: 256 x 256 tiles
+  int kind;    // 0: few rows (no LDS tile), 1: 128 x 128 tiles, 2: tiles of 256 columns x 128 rows
   int splits;  // parts of k
 };
 ScaledPlan scaled_plan(int64_t m, int64_t n, int64_t k);

@@ -3,8 +3,7 @@
 //
 //   C_ij = sum_b sa_ib sb_jb sum_{l in b} A_il B_jl.
 //
-// Every inner sum of 128 is one v_mfma_f32_16x16x128_f8f6f4 (hardware scales at
-// 1); its result is scaled and added to a float32 accumulator by the vector
+// Every inner sum of 128 is one v_mfma_f32_16x16x128_f8f6f4; its result is scaled and added to a float32 accumulator by the vector
 // units.  That instruction adds the products of eight steps on a common
 // exponent and keeps 17 bits below the largest (measured: next to 2^16 the
 // smallest product that counts is 2^0 among its eight, 2^-7 among the others),
@@ -17,6 +16,8 @@
 // square form) one per wave, and their product costs one multiplication per
 // column block beside one FMA per output.  The instruction's order of the 128
 // steps within a lane does not matter, since both operands use the same one.
+#include <type_traits>
+
 #include "tile_core.hpp"
 
 namespace mr {
@@ -31,7 +32,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 template <int QF>
 __device__ __forceinline__ v4f mfma8(v8i p, v8i q) {
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, zero, 0, QF, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, zero, 0, QF, 0, 0, 0, 0);  // zeros: the unscaled form
 }
 
 // The same 32 bytes per lane as fp16, and the sum of 128 steps as four of 32.
@@ -60,12 +61,6 @@ __device__ __forceinline__ Wide widen32(v8i x) {
   }
   return w;
 }
-__device__ __forceinline__ v4f mfma_wide(const Wide& p, const Wide& q) {
-  v4f d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[i], q.h[i], d, 0, 0, 0);
-  return d;
-}
 // Fragments of either kind.
 template <bool WIDE, int F>
 struct Frag8 {
@@ -77,142 +72,377 @@ struct Frag8<true, F> {
   typedef Wide type;
   static __device__ __forceinline__ Wide of(v8i x) { return widen32<F>(x); }
 };
-template <int QF>
-__device__ __forceinline__ v4f product(v8i p, v8i q) {
-  return mfma8<QF>(p, q);
+// d[i] = P Q_i^T for N column blocks (the fp16 form in four passes over the
+// blocks, so that no product waits for the one before it).
+template <int QF, int N>
+__device__ __forceinline__ void products(v8i p, const v8i (&q)[N], v4f (&d)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) d[i] = mfma8<QF>(p, q[i]);
 }
-template <int QF>
-__device__ __forceinline__ v4f product(const Wide& p, const Wide& q) {
-  return mfma_wide(p, q);
+template <int QF, int N>
+__device__ __forceinline__ void products(const Wide& p, const Wide (&q)[N], v4f (&d)[N]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const v4f zero = {0.f, 0.f, 0.f, 0.f};
+      d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[k], q[i].h[k], k == 0 ? zero : d[i], 0, 0, 0);
+    }
 }
 
 __device__ __forceinline__ v8i join(v4i a, v4i b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Fragment of rows row .. row + 15 of an LDS chunk: bytes 16 g and 64 + 16 g, g = lane / 16.
+// Fragment of rows row .. row + 15 (row a multiple of 16) of an LDS chunk: bytes
+// 16 g and 64 + 16 g, g = lane / 16.  The slots depend on row % 16 alone, so a
+// lane has two offsets for all fragments.
 __device__ __forceinline__ v8i frag8(const unsigned char* st, int row, int lane) {
-  const int r = row + (lane & 15), g = lane >> 4;
-  const v4i a = *reinterpret_cast<const v4i*>(st + (r * 8 + dl_slot(r, g, 8)) * 16);
-  const v4i b = *reinterpret_cast<const v4i*>(st + (r * 8 + dl_slot(r, g + 4, 8)) * 16);
+  const int r = lane & 15, g = lane >> 4;
+  const unsigned char* p = st + row * kChunkBytes;
+  const v4i a = *reinterpret_cast<const v4i*>(p + (r * 8 + dl_slot(r, g, 8)) * 16);
+  const v4i b = *reinterpret_cast<const v4i*>(p + (r * 8 + dl_slot(r, g + 4, 8)) * 16);
   return join(a, b);
 }
 
 }  // namespace
 
-template <int BP_, int BQ_, int WP_, int WQ_>
+template <int BP_, int BQ_, int WP_, int WQ_, int BPC_>
 struct ScaledShape {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NW = WP * WQ, THREADS = 64 * NW;
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NW = WP * WQ, BPC = BPC_, THREADS = 64 * NW;
   static constexpr int RB = BP / WP / 16, CB = BQ / WQ / 16;
   static constexpr int P_BYTES = BP * kChunkBytes, Q_BYTES = BQ * kChunkBytes;
-  static constexpr int STAGE = P_BYTES + Q_BYTES + BP * 4;  // P, Q, P's scales (vector form)
-  static constexpr int LDS = 2 * STAGE;
+  // P, Q, P's scales, Q's scales
+  static constexpr int SP = P_BYTES + Q_BYTES, SQ = SP + BP * 4, STAGE = SQ + BQ * 4;
+  static constexpr int NP = along_copies<BP, NW, 8>, NQ = along_copies<BQ, NW, 8>;  // copies per wave and chunk
+  static constexpr int NS = (BP + BQ + 64 * NW - 1) / (64 * NW);
+  static constexpr int COPIES = NP + NQ + NS;
+  static constexpr int SLABS = 2 * STAGE, LDS = SLABS + NW * Slab<float, 16>::BYTES;
+  static constexpr int WAVES_PER_SIMD = BPC * NW / 4;
+  static_assert(RB % 2 == 0 && BPC * LDS <= 160 * 1024, "the stages fit");
 };
 
+// One tile of C, or of one part of a split contraction.
+template <class S>
+struct ScaledTile {
+  int64_t q0;
+  int p0, pv, qv, part, c_begin, c_end;
+  __device__ __forceinline__ void load(const ScaledArgs& a, int id) {
+    const int tp = (a.n + S::BP - 1) / S::BP, tq = (int)((a.m + S::BQ - 1) / S::BQ);
+    part = id / (tp * tq);
+    int ti, tj;
+    full_tile_grouped(id % (tp * tq), tq, tp, ti, tj);
+    q0 = (int64_t)ti * S::BQ;
+    p0 = tj * S::BP;
+    pv = min(S::BP, a.n - p0);
+    qv = (int)min((int64_t)S::BQ, a.m - q0);
+    const int64_t chunks = (a.k + kChunkBytes - 1) / kChunkBytes;
+    c_begin = (int)(chunks * part / a.splits);
+    c_end = (int)(chunks * (part + 1) / a.splits);
+  }
+};
+
+// The chunks of a workgroup's tiles in order, for the copies (past the last one
+// it stays on that one).
+template <class S>
+struct ScaledFeed {
+  ScaledTile<S> t;
+  Walk w;
+  int c, units, left;
+  unsigned char* st;
+  const char *p, *q, *sp, *sq;
+  __device__ __forceinline__ ScaledFeed(const ScaledArgs& a, const Walk& w_) : w(w_) {
+    t.load(a, w.at);
+    c = t.c_begin;
+  }
+  // The current chunk goes to `stage`.
+  __device__ __forceinline__ void begin(const ScaledArgs& a, unsigned char* stage) {
+    st = stage;
+    const int64_t k0 = (int64_t)c * kChunkBytes;
+    left = (int)min((int64_t)kChunkBytes, a.k - k0);
+    units = (left + 15) >> 4;
+    p = wave_uniform(a.p + (int64_t)t.p0 * a.ldp + k0);
+    q = wave_uniform(a.q + t.q0 * a.ldq + k0);
+    sp = wave_uniform(a.sp + (int64_t)(t.p0 >> a.p_shift) * a.ldsp + c);
+    sq = wave_uniform(a.sq + (t.q0 >> a.q_shift) * a.ldsq + c);
+  }
+  // Copy j (0 .. COPIES - 1) of the wave.
+  __device__ __forceinline__ void copy(const ScaledArgs& a, int j, int wave, int lane) {
+    if (j < S::NP) {
+      copy_along_one<S::BP, S::NW, 8>(p, a.ldp, t.pv, units, st, wave, lane, j);
+    } else if (j < S::NP + S::NQ) {
+      copy_along_one<S::BQ, S::NW, 8>(q, a.ldq, t.qv, units, st + S::P_BYTES, wave, lane, j - S::NP);
+    } else {
+      // the scale of row i of P, then of Q, 64 rows to a copy (rows past the end repeat the last
+      // one, surplus copies the first ones); tiles start at multiples of 128 rows
+      const int first = (((j - S::NP - S::NQ) * S::NW + wave) * 64) % (S::BP + S::BQ);
+      const bool is_p = first < S::BP;
+      const int row = min(is_p ? first + lane : first - S::BP + lane, (is_p ? t.pv : t.qv) - 1);
+      uint32_t off = (uint32_t)(row >> (is_p ? a.p_shift : a.q_shift)) * (uint32_t)(is_p ? a.ldsp : a.ldsq) * 4u;
+      const char* s = is_p ? sp : sq;
+      asm volatile("" : "+v"(off));
+      asm volatile("" : "+s"(s));
+      __builtin_amdgcn_global_load_lds((global_void_ptr)(s + off), (lds_void_ptr)(st + S::SP + first * 4), 4, 0, 0);
+    }
+  }
+  // The current chunk has landed (and a barrier has passed): the bytes past the
+  // contraction's end become zeros, so that nothing that lies there reaches a sum.
+  __device__ __forceinline__ void clear_end() const {
+    for (int r = threadIdx.x; r < S::BP + S::BQ; r += S::THREADS) {
+#pragma unroll 1
+      for (int u = left >> 4; u < 8; ++u) {
+        v4u* unit = reinterpret_cast<v4u*>(st + (r * 8 + dl_slot(r, u, 8)) * 16);  // (BP rows of P, then Q's)
+        v4u x = {0, 0, 0, 0};
+        const int keep = left - 16 * u;
+        if (keep > 0) {
+          x = *unit;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int n = keep - 4 * d;
+            x[d] = n >= 4 ? x[d] : n <= 0 ? 0u : x[d] & ((1u << (8 * n)) - 1u);
+          }
+        }
+        *unit = x;
+      }
+    }
+  }
+  __device__ __forceinline__ void next(const ScaledArgs& a) {
+    if (++c < t.c_end) return;
+    if (w.at + w.step < w.end) {
+      w.at += w.step;
+      t.load(a, w.at);
+      c = t.c_begin;
+    } else {
+      --c;
+    }
+  }
+};
+
+// Rows of C (or of a part's partial sums) from the accumulators.
+template <class S, typename O>
+__device__ __forceinline__ void scaled_put(O* c, int64_t ldc, const ScaledTile<S>& t, bool vec, bool accumulate, int wp, int wq,
+                                           int lane, unsigned char* slab, const v4f (&acc)[S::RB][S::CB]) {
+  using W = Slab<O, 16>;
+  constexpr int RP = S::RB < W::COLS / 16 ? S::RB : W::COLS / 16;
+#pragma unroll
+  for (int cb = 0; cb < S::CB; ++cb) {
+    const int q = wq * (S::BQ / S::WQ) + cb * 16;
+#pragma unroll
+    for (int r0 = 0; r0 < S::RB; r0 += RP) {
+      const int p = wp * (S::BP / S::WP) + r0 * 16;
+#pragma unroll
+      for (int rb = 0; rb < RP; ++rb) {
+        const v4f& x = acc[r0 + rb][cb];
+        const float v[4] = {x[0], x[1], x[2], x[3]};
+        W::put4(slab, lane & 15, rb * 16 + 4 * (lane >> 4), v);
+      }
+      W::fence();
+      W::store(slab, c + (t.q0 + q) * ldc + t.p0 + p, ldc, t.qv - q, min(t.pv - p, RP * 16), vec, accumulate, lane);
+      W::fence();
+    }
+  }
+}
+
+// C in tiles, a workgroup's tiles one after another as one stream of chunks of
+// 128 steps through two stages of LDS: the next chunk (the next tile's first,
+// at a tile's end) is copied under this one's products, as soon as its stage is
+// free.  Every block of 16 x 16 results is scaled and added one step behind its
+// product, so that the vector units work under the next products.  The barrier
+// of the next chunk comes before a chunk's last step, whose fragments are in
+// registers by then; Q's fragments of the next chunk are read as the last
+// products release them.
 template <class S, int QF, bool PVEC, bool WIDE>
-__global__ __launch_bounds__(S::THREADS) void scaled_tile_kernel(const ScaledArgs a) {
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_kernel(const ScaledArgs a) {
+  extern __shared__ __align__(256) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = ((a.n + S::BP - 1) / S::BP) * (int)((a.m + S::BQ - 1) / S::BQ) * a.splits;
+  Walk w(tiles);
+  if (w.at >= w.end) return;
+  const int wp = wave / S::WQ, wq = wave % S::WQ;
+  const int prow = wp * (S::BP / S::WP), qrow = wq * (S::BQ / S::WQ);
+  unsigned char* slab = lds + S::SLABS + wave * Slab<float, 16>::BYTES;
+  using FP = Frag8<WIDE, 0>;
+  using FQ = Frag8<WIDE, QF>;
+  v8i raw;                    // P's fragment of the next step
+  typename FQ::type fq[S::CB];
+  float sc[S::CB], sc_old[S::CB];  // Q's scales (times P's in the square form) of this chunk and the last one
+  f4 sr, sr_old;                   // P's scales of a step's four rows (vector form), and the step's before
+  int g = 0;                       // chunk of the stream, in stage g & 1
+  auto read_q = [&](const unsigned char* st, int cb) { return FQ::of(frag8(st + S::P_BYTES, qrow + cb * 16, lane)); };
+  auto read_scales = [&](const unsigned char* st) {
+    const float* sp = reinterpret_cast<const float*>(st + S::SP);
+    const float* sq = reinterpret_cast<const float*>(st + S::SQ);
+#pragma unroll
+    for (int cb = 0; cb < S::CB; ++cb) sc[cb] = sq[qrow + cb * 16 + (lane & 15)];
+    if (!PVEC) {
+      const float s = sp[prow];  // the wave's rows of P lie in one square
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) sc[cb] *= s;
+    }
+  };
+  auto read_sr = [&](const unsigned char* st, int rb) {
+    if (PVEC) sr = *reinterpret_cast<const f4*>(st + S::SP + (prow + rb * 16 + 4 * (lane >> 4)) * 4);
+  };
+  ScaledFeed<S> feed(a, w);
+  auto land = [&] {  // the chunk being copied is in LDS; every wave has read the one before
+    stage_barrier();
+    if (feed.left < kChunkBytes) {
+      feed.clear_end();
+      stage_barrier();
+    }
+  };
+  feed.begin(a, lds);
+#pragma unroll
+  for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+  land();
+  feed.next(a);
+  feed.begin(a, lds + S::STAGE);
+#pragma unroll
+  for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+#pragma unroll
+  for (int cb = 0; cb < S::CB; ++cb) fq[cb] = read_q(lds, cb);
+  raw = frag8(lds, prow, lane);
+  read_scales(lds);
+  for (; w.at < w.end; w.at += w.step) {
+    ScaledTile<S> t;
+    t.load(a, w.at);
+    v4f acc[S::RB][S::CB], d[S::CB];
+#pragma unroll
+    for (int rb = 0; rb < S::RB; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) acc[rb][cb] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int cb = 0; cb < S::CB; ++cb) {
+      d[cb] = {0.f, 0.f, 0.f, 0.f};
+      sc_old[cb] = 0.f;
+    }
+    sr = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int rb, int cb, float q, const f4& r) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        acc[rb][cb][v] = PVEC ? fmaf(d[cb][v] * q, r[v], acc[rb][cb][v]) : fmaf(d[cb][v], q, acc[rb][cb][v]);
+      // done here: left free, the compiler gathers the additions behind all products, with all of
+      // their results in registers
+      asm volatile("" : "+v"(acc[rb][cb]));
+    };
+    for (int c = t.c_begin; c < t.c_end; ++c) {
+      unsigned char* st = lds + (g & 1) * S::STAGE;
+      const unsigned char* other = lds + ((g + 1) & 1) * S::STAGE;
+#pragma unroll
+      for (int rb = 0; rb < S::RB; ++rb) {
+        const bool last = rb + 1 == S::RB;
+        const typename FP::type fp = FP::of(raw);
+        sr_old = sr;
+        read_sr(st, rb);
+        if (last) {
+          land();
+          raw = frag8(other, prow, lane);  // (past the stream's end: stale bytes that nothing uses)
+          // this chunk's stage is free at once: the chunk after the next goes there
+          feed.next(a);
+          feed.begin(a, st);
+#pragma unroll
+          for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+        } else {
+          raw = frag8(st, prow + (rb + 1) * 16, lane);
+        }
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int cb = 0; cb < S::CB; ++cb) add(rb == 0 ? S::RB - 1 : rb - 1, cb, rb == 0 ? sc_old[cb] : sc[cb], sr_old);
+          products<QF>(fp, fq, d);
+          if (last) {
+#pragma unroll
+            for (int cb = 0; cb < S::CB; ++cb) fq[cb] = read_q(other, cb);
+          }
+        } else {
+#pragma unroll
+          for (int cb = 0; cb < S::CB; ++cb) {
+            add(rb == 0 ? S::RB - 1 : rb - 1, cb, rb == 0 ? sc_old[cb] : sc[cb], sr_old);
+            d[cb] = mfma8<QF>(fp, fq[cb]);
+            if (last) fq[cb] = read_q(other, cb);
+            __builtin_amdgcn_sched_barrier(0);  // keep the order: it bounds the registers
+          }
+        }
+        if (last) {
+#pragma unroll
+          for (int cb = 0; cb < S::CB; ++cb) sc_old[cb] = sc[cb];
+          read_scales(other);
+        }
+      }
+      ++g;
+    }
+#pragma unroll
+    for (int cb = 0; cb < S::CB; ++cb) add(S::RB - 1, cb, sc_old[cb], sr);
+    if (S::BP == 128 && a.partial)  // only the small tiles split the contraction
+      scaled_put<S>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
+    else if constexpr (WIDE)
+      scaled_put<S>(reinterpret_cast<float*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+    else if (a.c_type == MR_F16)
+      scaled_put<S>(reinterpret_cast<_Float16*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+    else
+      scaled_put<S>(reinterpret_cast<bf16_t*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+  }
+  wait_vmcnt<0>();  // the surplus copies of the last chunk: LDS is given back after them
+}
+
+// The general form, for operands whose rows are not whole 16-byte units: tiles
+// of 128 x 128, every element of an operand checked, one stage, no overlap.
+// Products and sums in the order of the form above.
+template <int QF, bool PVEC, bool WIDE>
+__global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
+  using S = ScaledShape<128, 128, 2, 2, 1>;
   extern __shared__ __align__(256) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / S::WQ, wq = wave % S::WQ;
-  const int tp = (a.n + S::BP - 1) / S::BP;
-  const int tq = (int)((a.m + S::BQ - 1) / S::BQ);
-  int ti, tj;
-  full_tile_grouped((int)xcd_remap(blockIdx.x, gridDim.x), tq, tp, ti, tj);
-  const int64_t q0 = (int64_t)ti * S::BQ;
-  const int p0 = tj * S::BP;
-  const int pv = min(S::BP, a.n - p0), qv = (int)min((int64_t)S::BQ, a.m - q0);
-  const int chunks = (a.k + kChunkBytes - 1) / kChunkBytes;
-  const int c_begin = (int)((int64_t)chunks * blockIdx.y / a.splits);
-  const int c_end = (int)((int64_t)chunks * (blockIdx.y + 1) / a.splits);
-
+  const int prow = wp * 64, qrow = wq * 64;
+  ScaledTile<S> t;
+  t.load(a, blockIdx.x);
   v4f acc[S::RB][S::CB];
 #pragma unroll
   for (int rb = 0; rb < S::RB; ++rb)
 #pragma unroll
     for (int cb = 0; cb < S::CB; ++cb) acc[rb][cb] = {0.f, 0.f, 0.f, 0.f};
-
-  const float* sq[S::CB];
-#pragma unroll
-  for (int cb = 0; cb < S::CB; ++cb) {
-    const int64_t r = q0 + min(wq * (S::BQ / S::WQ) + cb * 16 + (lane & 15), qv - 1);
-    sq[cb] = a.sq + (r >> a.q_shift) * a.ldsq;
-  }
-  // square form: the wave's rows of P lie in one 128-block of scales
-  const float* sp = a.sp + (int64_t)((p0 + wp * (S::BP / S::WP)) / kBlock) * a.ldsp;
-  if (!PVEC && p0 + wp * (S::BP / S::WP) >= a.n) sp = a.sp;
-
-  auto issue = [&](int c) {
-    unsigned char* st = lds + (c & 1) * S::STAGE;
+  for (int c = t.c_begin; c < t.c_end; ++c) {
     const int64_t k0 = (int64_t)c * kChunkBytes;
-    const int left = a.k - (int)k0;
-    if (a.fast && left >= kChunkBytes) {
-      copy_along<S::BP, S::NW, 8>(a.p, a.ldp, p0, pv, k0, 8, st, wave, lane);
-      copy_along<S::BQ, S::NW, 8>(a.q, a.ldq, q0, qv, k0, 8, st + S::P_BYTES, wave, lane);
-    } else {
-      edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, p0, pv, k0, left, a.fast, st, threadIdx.x);
-      edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, q0, qv, k0, left, a.fast, st + S::P_BYTES, threadIdx.x);
-    }
-    if (PVEC) {
-      float* s = reinterpret_cast<float*>(st + S::P_BYTES + S::Q_BYTES);
-      for (int t = threadIdx.x; t < S::BP; t += S::THREADS) s[t] = t < pv ? a.sp[(int64_t)(p0 + t) * a.ldsp + c] : 0.f;
-    }
-  };
-
-  if (c_begin < c_end) issue(c_begin);
-  for (int c = c_begin; c < c_end; ++c) {
+    const int left = (int)min((int64_t)kChunkBytes, a.k - k0);
+    __syncthreads();
+    edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, t.p0, t.pv, k0, left, false, lds, threadIdx.x);
+    edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, t.q0, t.qv, k0, left, false, lds + S::P_BYTES, threadIdx.x);
+    __syncthreads();
+    typename Frag8<WIDE, QF>::type fq[S::CB];
     float sc[S::CB];
 #pragma unroll
-    for (int cb = 0; cb < S::CB; ++cb) sc[cb] = sq[cb][c];
-    if (!PVEC) {
-      const float s = sp[c];
-#pragma unroll
-      for (int cb = 0; cb < S::CB; ++cb) sc[cb] *= s;
+    for (int cb = 0; cb < S::CB; ++cb) {
+      fq[cb] = Frag8<WIDE, QF>::of(frag8(lds + S::P_BYTES, qrow + cb * 16, lane));
+      const int64_t r = t.q0 + min(qrow + cb * 16 + (lane & 15), t.qv - 1);
+      sc[cb] = a.sq[(r >> a.q_shift) * a.ldsq + c];
+      if (!PVEC) sc[cb] *= a.sp[(int64_t)(t.p0 >> a.p_shift) * a.ldsp + c];
     }
-    stage_barrier();  // chunk c is in LDS; every wave is done with chunk c - 1
-    if (c + 1 < c_end) issue(c + 1);
-    const unsigned char* st = lds + (c & 1) * S::STAGE;
-    typename Frag8<WIDE, QF>::type fq[S::CB];
-#pragma unroll
-    for (int cb = 0; cb < S::CB; ++cb)
-      fq[cb] = Frag8<WIDE, QF>::of(frag8(st + S::P_BYTES, wq * (S::BQ / S::WQ) + cb * 16, lane));
 #pragma unroll
     for (int rb = 0; rb < S::RB; ++rb) {
-      const int row = wp * (S::BP / S::WP) + rb * 16;
-      const typename Frag8<WIDE, 0>::type fp = Frag8<WIDE, 0>::of(frag8(st, row, lane));
       v4f d[S::CB];
+      const typename Frag8<WIDE, 0>::type fp = Frag8<WIDE, 0>::of(frag8(lds, prow + rb * 16, lane));
+      products<QF>(fp, fq, d);
 #pragma unroll
-      for (int cb = 0; cb < S::CB; ++cb) d[cb] = product<QF>(fp, fq[cb]);
-      if (PVEC) {
-        const f4 s = *reinterpret_cast<const f4*>(st + S::P_BYTES + S::Q_BYTES + (row + 4 * (lane >> 4)) * 4);
-#pragma unroll
-        for (int cb = 0; cb < S::CB; ++cb)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[rb][cb][v] = fmaf(d[cb][v] * sc[cb], s[v], acc[rb][cb][v]);
-      } else {
+      for (int v = 0; v < 4; ++v) {
+        const int r = t.p0 + min(prow + rb * 16 + 4 * (lane >> 4) + v, t.pv - 1);
+        const float s = PVEC ? a.sp[(int64_t)r * a.ldsp + c] : 1.f;
 #pragma unroll
         for (int cb = 0; cb < S::CB; ++cb)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[rb][cb][v] = fmaf(d[cb][v], sc[cb], acc[rb][cb][v]);
+          acc[rb][cb][v] = PVEC ? fmaf(d[cb][v] * sc[cb], s, acc[rb][cb][v]) : fmaf(d[cb][v], sc[cb], acc[rb][cb][v]);
       }
     }
   }
-
-#pragma unroll
-  for (int cb = 0; cb < S::CB; ++cb) {
-    const int qr = wq * (S::BQ / S::WQ) + cb * 16 + (lane & 15);
-    if (qr >= qv) continue;
-#pragma unroll
-    for (int rb = 0; rb < S::RB; ++rb) {
-      const int pr = wp * (S::BP / S::WP) + rb * 16 + 4 * (lane >> 4);
-      if (pr >= pv) continue;
-      const float v[4] = {acc[rb][cb][0], acc[rb][cb][1], acc[rb][cb][2], acc[rb][cb][3]};
-      if (a.partial)
-        put4(a.partial + ((int64_t)blockIdx.y * a.m + q0 + qr) * a.n + p0 + pr, v, pv - pr, a.n % 4 == 0, false);
-      else
-        put4_as(a.c, (q0 + qr) * a.ldc + p0 + pr, v, pv - pr, a.c_type, a.vec_c, a.accumulate);
-    }
-  }
+  unsigned char* slab = lds + S::P_BYTES + S::Q_BYTES + wave * Slab<float, 16>::BYTES;
+  if (a.partial)
+    scaled_put<S>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
+  else if constexpr (WIDE)
+    scaled_put<S>(reinterpret_cast<float*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+  else if (a.c_type == MR_F16)
+    scaled_put<S>(reinterpret_cast<_Float16*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+  else
+    scaled_put<S>(reinterpret_cast<bf16_t*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
 }
 
 // Few rows of C (m <= 16 CB): no tile in LDS.  A workgroup of NW waves owns 16
@@ -253,7 +483,10 @@ __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a
     for (int cb = 0; cb < CB; ++cb) {
       const int64_t r = min((int64_t)(cb * 16 + i), a.m - 1);
       const float sc = a.sq[(r >> a.q_shift) * a.ldsq + c];
-      const v4f d = product<QF>(fp, Frag8<WIDE, QF>::of(frag(a.q + r * a.ldq, c)));
+      v4f d1[1];
+      const typename Frag8<WIDE, QF>::type fq[1] = {Frag8<WIDE, QF>::of(frag(a.q + r * a.ldq, c))};
+      products<QF>(fp, fq, d1);
+      const v4f d = d1[0];
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[cb][v] = fmaf(d[v], sc * s[PVEC ? v : 0], acc[cb][v]);
     }
@@ -294,8 +527,9 @@ __global__ __launch_bounds__(256) void scaled_join_kernel(const ScaledArgs a) {
 // ------------------------------------------------------------ launchers
 namespace {
 
-using Tile128 = ScaledShape<128, 128, 2, 2>;
-using Tile256 = ScaledShape<256, 256, 2, 4>;
+using TileLarge = ScaledShape<256, 256, 2, 4, 1>;  // 16-bit C
+using TileWide = ScaledShape<256, 128, 4, 2, 1>;   // float32 C (fp16 fragments) or P's scales by row: more registers
+using Tile128 = ScaledShape<128, 128, 2, 2, 2>;
 constexpr int kFewRows = 64;
 constexpr int kCus = 256;
 
@@ -308,9 +542,17 @@ hipError_t go_tile(const ScaledArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     raised = true;
   }
-  const int64_t tiles = (int64_t)((a.n + S::BP - 1) / S::BP) * ((a.m + S::BQ - 1) / S::BQ);
-  hipLaunchKernelGGL((scaled_tile_kernel<S, QF, PVEC, WIDE>), dim3((unsigned)tiles, a.splits), dim3(S::THREADS), S::LDS, s,
-                     a);
+  const int64_t tiles = (int64_t)((a.n + S::BP - 1) / S::BP) * ((a.m + S::BQ - 1) / S::BQ) * a.splits;
+  hipLaunchKernelGGL((scaled_tile_kernel<S, QF, PVEC, WIDE>), dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS),
+                     S::LDS, s, a);
+  return hipGetLastError();
+}
+
+template <int QF, bool PVEC, bool WIDE>
+hipError_t go_edge(const ScaledArgs& a, hipStream_t s) {
+  const int64_t tiles = (int64_t)((a.n + 127) / 128) * ((a.m + 127) / 128) * a.splits;
+  constexpr int bytes = 256 * kChunkBytes + 4 * Slab<float, 16>::BYTES;
+  hipLaunchKernelGGL((scaled_edge_kernel<QF, PVEC, WIDE>), dim3((unsigned)tiles), dim3(256), bytes, s, a);
   return hipGetLastError();
 }
 
@@ -323,8 +565,8 @@ hipError_t go_rows(const ScaledArgs& a, hipStream_t s) {
 
 template <int QF, bool PVEC, bool WIDE>
 hipError_t go_kind(const ScaledArgs& a, int kind, hipStream_t s) {
-  if constexpr (!WIDE)
-    if (kind == 2) return go_tile<Tile256, QF, PVEC, WIDE>(a, s);
+  if (kind >= 1 && !a.fast) return go_edge<QF, PVEC, WIDE>(a, s);
+  if (kind == 2) return go_tile<std::conditional_t<WIDE || PVEC, TileWide, TileLarge>, QF, PVEC, WIDE>(a, s);
   if (kind >= 1) return go_tile<Tile128, QF, PVEC, WIDE>(a, s);
   if (a.m <= 16) return go_rows<1, QF, PVEC, WIDE>(a, s);
   if (a.m <= 32) return go_rows<2, QF, PVEC, WIDE>(a, s);
@@ -341,9 +583,9 @@ hipError_t go_width(const ScaledArgs& a, int kind, hipStream_t s) {
 ScaledPlan scaled_plan(int64_t m, int64_t n, int64_t k) {
   if (m <= kFewRows) return {0, 1};
   const int64_t chunks = (k + kChunkBytes - 1) / kChunkBytes;
-  auto tiles = [&](int b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
-  if (tiles(256) >= kCus) return {2, 1};
-  const int64_t t = tiles(128);
+  auto tiles = [&](int p, int q) { return ((m + q - 1) / q) * ((n + p - 1) / p); };
+  if (tiles(256, 256) >= kCus) return {2, 1};
+  const int64_t t = tiles(128, 128);
   int64_t splits = 1;
   while (splits < 16 && t * splits * 2 <= 2 * kCus && chunks / (splits * 2) >= 8) splits *= 2;
   return {1, (int)splits};

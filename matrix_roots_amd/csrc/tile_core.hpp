@@ -31,19 +31,26 @@ __device__ __forceinline__ int across_swap(int row) {
 // never stored.  Units past the first `units` re-read the last one: the reader
 // masks those steps.
 template <int R, int NW, int UPR>
+constexpr int along_copies = R * UPR / 64 / NW;  // per wave
+// Copy j of a wave; p: the chunk's first byte of the tile's first row.
+template <int R, int NW, int UPR>
+__device__ __forceinline__ void copy_along_one(const char* p, int64_t ld_bytes, int valid, int units, unsigned char* stage,
+                                               int wave, int lane, int j) {
+  static_assert(along_copies<R, NW, UPR> * 64 * NW == R * UPR, "copies cover the chunk");
+  const int u0 = (j * NW + wave) * 64;
+  const int u = u0 + lane, row = u / UPR;
+  uint32_t off = (uint32_t)min(row, valid - 1) * (uint32_t)ld_bytes +
+                 (uint32_t)(min(dl_slot(row, u % UPR, UPR), units - 1) * 16);
+  asm volatile("" : "+v"(off));  // opaque per copy: the offset stays a 32-bit lane value
+  __builtin_amdgcn_global_load_lds((global_void_ptr)(p + off), (lds_void_ptr)(stage + u0 * 16), 16, 0, 0);
+}
+template <int R, int NW, int UPR>
 __device__ __forceinline__ void copy_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
                                            int units, unsigned char* stage, int wave, int lane) {
-  constexpr int N = R * UPR / 64 / NW;
-  static_assert(N * 64 * NW == R * UPR, "copies cover the chunk");
   const char* p = wave_uniform(base + row0 * ld_bytes + k0);
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int u0 = (j * NW + wave) * 64;
-    const int u = u0 + lane, row = u / UPR;
-    uint32_t off = (uint32_t)min(row, valid - 1) * (uint32_t)ld_bytes + (uint32_t)(min(dl_slot(row, u % UPR, UPR), units - 1) * 16);
-    asm volatile("" : "+v"(off));  // opaque per copy: the offset stays a 32-bit lane value
-    __builtin_amdgcn_global_load_lds((global_void_ptr)(p + off), (lds_void_ptr)(stage + u0 * 16), 16, 0, 0);
-  }
+  for (int j = 0; j < along_copies<R, NW, UPR>; ++j)
+    copy_along_one<R, NW, UPR>(p, ld_bytes, valid, units, stage, wave, lane, j);
 }
 
 // A chunk of an `across` tile: contraction rows k0 .. k0 + BK - 1, the R columns
@@ -88,6 +95,7 @@ __device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n, bool ali
 template <int R, int THREADS, int ES, int UPR>
 __device__ __forceinline__ void edge_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
                                            int k_left, bool aligned, unsigned char* stage, int thread) {
+#pragma unroll 1
   for (int u = thread; u < R * UPR; u += THREADS) {
     const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
@@ -99,6 +107,7 @@ template <int R, int THREADS, int BK>
 __device__ __forceinline__ void edge_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int k_left, int64_t col0,
                                             int valid, bool aligned, unsigned char* stage, int thread) {
   constexpr int UPR = R / 8;
+#pragma unroll 1
   for (int u = thread; u < BK * UPR; u += THREADS) {
     const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
@@ -145,12 +154,12 @@ __device__ __forceinline__ void put4_as(void* c, int64_t at, const float (&v)[4]
     put4(reinterpret_cast<bf16_t*>(c) + at, v, left, vec, accumulate);
 }
 
-// 32 rows of outputs of one wave through LDS, so that they leave in 16-byte
+// ROWS rows of outputs of one wave through LDS, so that they leave in 16-byte
 // units: 128 bytes of O to a row, unit u of row r in slot u ^ (r % 8).  The
 // wave's LDS instructions run in order, so only the compiler has to keep them so.
-template <typename O>
+template <typename O, int ROWS>
 struct Slab {
-  static constexpr int COLS = 128 / (int)sizeof(O), BYTES = 32 * 128, EU = 16 / (int)sizeof(O);
+  static constexpr int COLS = 128 / (int)sizeof(O), BYTES = ROWS * 128, EU = 16 / (int)sizeof(O);
   static __device__ __forceinline__ void put4(unsigned char* slab, int row, int col, const float (&v)[4]) {
     O t[4];
 #pragma unroll
@@ -175,7 +184,7 @@ struct Slab {
   static __device__ __forceinline__ void store(const unsigned char* slab, O* c, int64_t ldc, int rows_left, int cols_left,
                                                bool vec, bool accumulate, int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < ROWS / 8; ++j) {
       const int row = 8 * j + (lane >> 3), unit = lane & 7, col = unit * EU;
       if (row >= rows_left || col >= cols_left) continue;
       const v4u x = *reinterpret_cast<const v4u*>(slab + row * 128 + (unit ^ (row & 7)) * 16);
@@ -193,9 +202,70 @@ struct Slab {
   }
 };
 
-// This wave's copies and LDS stores are done, and so are every other wave's.
+// This wave's copies and LDS operations are done, and so are every other wave's.
 __device__ __forceinline__ void stage_barrier() {
   wait_vmcnt<0>();
+  wait_lgkmcnt0();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tiles of a persistent workgroup: tile k of slot b / 8 on XCD b % 8, where
+// every XCD owns one run of `total` / 8 tiles and walks it in order, so that
+// the tiles in flight on an XCD are neighbours and share operands in its L2.
+struct Walk {
+  int at, step, end;
+  __device__ __forceinline__ Walk(int total) {
+    const int x = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
+    end = (int)((int64_t)total * (x + 1) / kNumXcd);
+    at = (int)((int64_t)total * x / kNumXcd) + blockIdx.x / kNumXcd;
+    step = slots;
+  }
+};
+// Workgroups of a launch over at most `tiles` tiles: what the CUs hold at a
+// time, a multiple of the XCDs.
+inline unsigned persistent_blocks(int64_t tiles, int per_cu) {
+  const int64_t most = 256 * per_cu;
+  return (unsigned)(tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most);
+}
+
+// Wave roles of a streamed kernel: the last kLoaders waves of a workgroup copy
+// operands to LDS, the others multiply and store.
+constexpr int kLoaders = 4;
+
+// The loader waves' side of a stream of chunks through NST stages, COPIES direct
+// copies a wave and chunk.  issue(j) puts the stream's chunk j into stage j %
+// NST: 1 by direct copies only, 0 with LDS stores among them, -1 past the end.
+// One barrier per chunk: before it the loaders wait for that chunk's copies
+// alone, after it the stage of its predecessor is free.
+template <int NST, int COPIES, class Issue>
+__device__ __forceinline__ void copy_chunks(Issue&& issue) {
+  static_assert((NST - 2) * COPIES < 64, "the wait counts to 63");
+  int issued = 0, stored = -1;  // chunks issued, the last one with LDS stores
+  auto next = [&] {
+    const int r = issue(issued);
+    if (r < 0) return false;
+    if (r == 0) stored = issued;
+    ++issued;
+    return true;
+  };
+  for (int i = 0; i < NST - 1; ++i) next();
+  for (int j = 0;; ++j) {
+    // chunk j has landed once at most the copies of the NST - 2 after it are in flight
+    if (issued - 1 - j == NST - 2 && stored <= j)
+      wait_vmcnt<(NST - 2) * COPIES>();
+    else
+      wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // chunk j is in LDS; every wave is done with chunk j - 1
+    asm volatile("" ::: "memory");
+    if (!next() && j == issued) return;
+  }
+}
+// The other waves' barrier of a chunk.
+__device__ __forceinline__ void join_chunk() {
   wait_lgkmcnt0();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();

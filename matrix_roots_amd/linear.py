@@ -197,6 +197,12 @@ def _scales(name, s, rows, k):
     return B.MR_BLOCK_SQUARE, _ld(s)
 
 
+def _padded(t, ld) -> bool:
+    """Whether the last row's bytes up to a multiple of 16 lie in t's memory too."""
+    end = t.storage_offset() + (t.shape[0] - 1) * ld + (t.shape[1] + 15) // 16 * 16
+    return end <= t.untyped_storage().nbytes()
+
+
 def block_scaled_matmul(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, accumulate: bool = False, stream=None):
     """a b^T for 8-bit a (m, k) and b (n, k) with scales per block of 128 of k:
     sa (m, ceil(k / 128)) or (ceil(m / 128), ceil(k / 128)), sb alike.  a: e4m3
@@ -218,9 +224,11 @@ def block_scaled_matmul(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, accumu
         out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _same_shape("out", out, (m, n))
-    p = B.ScaledMatmulProblem(m, n, k, _ptr(a), _ld(a), _ptr(sa), ldsa, _ptr(b), _ld(b), _ptr(sb), ldsb, _ptr(out),
+    lda, ldb = _ld(a), _ld(b)
+    padded = k % 16 != 0 and _padded(a, lda) and _padded(b, ldb)
+    p = B.ScaledMatmulProblem(m, n, k, _ptr(a), lda, _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), ldsb, _ptr(out),
                               _ld(out), _EIGHTS[a.dtype], _EIGHTS[b.dtype], _float_code(out, "out"), a_block, b_block,
-                              1 if accumulate else 0)
+                              1 if accumulate else 0, 1 if padded else 0, 0)
     lib = library()
     need = lib.block_scaled_matmul_workspace(addressof(p))
     ws = _workspace(need, dev)
