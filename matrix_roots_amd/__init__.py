@@ -30,7 +30,7 @@ def __getattr__(name):
     if name in _LINEAR:
         from . import linear
 
-        return getattr(linear, name)
+        return globals().setdefault(name, getattr(linear, name))
     if name in __all__:
         from . import binding
 

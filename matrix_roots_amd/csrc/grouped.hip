@@ -145,19 +145,19 @@ struct Operand {
 
 // One operand's part of a chunk, by the loader waves.
 template <class S, int R, bool ACROSS>
-__device__ __forceinline__ void stage_operand(const Operand& o, bool direct, bool aligned, int64_t k0, int left,
+__device__ __forceinline__ void stage_operand(const Operand& o, bool direct, int64_t k0, int left,
                                               unsigned char* st, int loader, int lane) {
   const int thread = loader * 64 + lane;
   if constexpr (ACROSS) {
     if (direct)
       copy_across<R, kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, loader, lane);
     else
-      edge_across<R, 64 * kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, aligned, st, thread);
+      edge_across<R, 64 * kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, thread);
   } else {
     if (direct)
       copy_along<R, kLoaders, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, (left + 7) / 8, st, loader, lane);
     else
-      edge_along<R, 64 * kLoaders, 2, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, left, aligned, st, thread);
+      edge_along<R, 64 * kLoaders, 2, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, left, st, thread);
   }
 }
 
@@ -219,7 +219,7 @@ struct Tile {
 
 // The loader waves' side of stream_tiles.
 template <class S, bool PA, bool QA, class Load>
-__device__ __forceinline__ void copy_stream(Walk w, bool fast, unsigned char* lds, Load&& load, int loader, int lane) {
+__device__ __forceinline__ void copy_stream(Walk w, unsigned char* lds, Load&& load, int loader, int lane) {
   Tile<S> t;
   t.chunks = 0;
   int c = 0;  // next chunk of t
@@ -233,8 +233,8 @@ __device__ __forceinline__ void copy_stream(Walk w, bool fast, unsigned char* ld
     unsigned char* st = lds + j % S::NST * S::STAGE;
     const int64_t k0 = (int64_t)c * S::BK;
     const int left = (int)min((int64_t)S::BK, t.steps - k0);
-    stage_operand<S, S::BP, PA>(t.P, t.direct, fast, k0, left, st, loader, lane);
-    stage_operand<S, S::BQ, QA>(t.Q, t.direct, fast, k0, left, st + S::P_BYTES, loader, lane);
+    stage_operand<S, S::BP, PA>(t.P, t.direct, k0, left, st, loader, lane);
+    stage_operand<S, S::BQ, QA>(t.Q, t.direct, k0, left, st + S::P_BYTES, loader, lane);
     ++c;
     return t.direct ? 1 : 0;
   });
@@ -249,11 +249,11 @@ __device__ __forceinline__ void copy_stream(Walk w, bool fast, unsigned char* ld
 // end of the stream.  load(tile, id) describes tile `id`, put(tile, acc, slab)
 // stores one.
 template <class S, typename T, bool PA, bool QA, class Load, class Put>
-__device__ __forceinline__ void stream_tiles(Walk w, bool fast, unsigned char* lds, Load&& load, Put&& put) {
+__device__ __forceinline__ void stream_tiles(Walk w, unsigned char* lds, Load&& load, Put&& put) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= S::NW) {
-    copy_stream<S, PA, QA>(w, fast, lds, load, wave - S::NW, lane);
+    copy_stream<S, PA, QA>(w, lds, load, wave - S::NW, lane);
     return;
   }
   const int wp = wave / S::WQ, wq = wave % S::WQ;
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_ke
     else
       put_rows<S, T>(a, t.q0, t.qv, t.p0, t.pv, slab, acc);
   };
-  stream_tiles<S, T, TRANSPOSE, false>(Walk(tiles.total), a.fast, lds, load, put);
+  stream_tiles<S, T, TRANSPOSE, false>(Walk(tiles.total), lds, load, put);
   // rows of no expert: before the first and after the last offset
   const int64_t first = offset_at(a, 0), last = max(offset_at(a, a.experts), first);
   const int es = a.y_f32 ? 4 : 2;
@@ -448,22 +448,16 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_
     else
       put_weight<S>(a, reinterpret_cast<T*>(a.y) + t.e * a.y_stride, t.p0, t.pv, (int)t.q0, t.qv, acc);
   };
-  stream_tiles<S, T, true, true>(Walk(a.experts * tp * tq), a.fast, lds, load, put);
+  stream_tiles<S, T, true, true>(Walk(a.experts * tp * tq), lds, load, put);
 }
 
 // ------------------------------------------------------------ launchers
 namespace {
 
-#ifndef RWS
-#define RWS 256, 128, 2, 2, 64, 3, 1
-#endif
-#ifndef WSH
-#define WSH 256, 128, 2, 2, 64, 3, 1
-#endif
-using RowsWide = GroupedShape<RWS>;
+using RowsWide = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
 using RowsNarrow = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
 using RowsFew = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
-using Weights = GroupedShape<WSH>;
+using Weights = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
 
 template <class K>
 hipError_t raise_lds(K kernel, int bytes, bool& raised) {

@@ -119,11 +119,8 @@ mr_status rms_norm_forward(const mr_rms_norm_problem* p, void* hip_stream) {
   a.q = static_cast<unsigned char*>(p->q), a.ldq = p->ldq;
   a.s = p->scales, a.lds = p->lds;
   a.width = (int32_t)w, a.rows = p->rows, a.eps = (float)p->eps, a.e5m2 = p->q_dtype == MR_E5M2;
-  const bool vec = w % 8 == 0 && units16(p->x, p->ldx, es) && aligned(p->weight, 16) &&
-                   (!p->residual || (units16(p->residual, p->ldres, es) && units16(p->h, p->ldh, es))) &&
-                   (!p->y || units16(p->y, p->ldy, es)) && (!p->q || (aligned(p->q, 8) && p->ldq % 8 == 0));
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  return traced(kTrNorm, true, s, [&] { return launch_norm_forward(a, p->dtype, vec, s); }, "norm forward launch");
+  return traced(kTrNorm, true, s, [&] { return launch_norm_forward(a, p->dtype, s); }, "norm forward launch");
 }
 
 size_t rms_norm_backward_workspace(const mr_rms_norm_grad_problem* p) {
@@ -176,9 +173,7 @@ mr_status rms_norm_backward(const mr_rms_norm_grad_problem* p, void* ws, size_t 
     a.y = p->dx, a.ldy = p->lddx;
     a.partial = partial;
     a.width = (int32_t)w, a.rows = p->rows;
-    const bool vec = w % 8 == 0 && units16(p->dy, p->lddy, es) && units16(p->h, p->ldh, es) && aligned(p->weight, 16) &&
-                     (!p->dresidual || units16(p->dresidual, p->ldres, es)) && units16(p->dx, p->lddx, es);
-    MR_TRY(traced(kTrNormGrad, true, s, [&] { return launch_norm_backward(a, p->dtype, vec, blocks, s); },
+    MR_TRY(traced(kTrNormGrad, true, s, [&] { return launch_norm_backward(a, p->dtype, blocks, s); },
                   "norm backward launch"));
   }
   if (!p->dweight) return MR_OK;
@@ -224,11 +219,8 @@ mr_status quantize_blocks(const mr_quantize_problem* p, void* hip_stream) {
   a.qt = static_cast<unsigned char*>(p->QT), a.ldqt = p->ldqt, a.st = p->ST, a.ldst = p->ldst;
   a.m = p->m, a.n = (int32_t)p->n;
   a.square = square, a.e5m2 = p->q_dtype == MR_E5M2;
-  a.vec_q = p->Q && aligned(p->Q, 8) && p->ldq % 8 == 0;
-  a.vec_qt = p->QT && aligned(p->QT, 16) && p->ldqt % 16 == 0;
-  const bool vec = p->n % 8 == 0 && units16(p->X, p->ldx, es);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  return traced(kTrQuantize, true, s, [&] { return launch_quantize(a, p->x_dtype, vec, s); }, "quantize launch");
+  return traced(kTrQuantize, true, s, [&] { return launch_quantize(a, p->x_dtype, s); }, "quantize launch");
 }
 
 // --------------------------------------------------- block-scaled product

@@ -33,10 +33,9 @@ struct NormArgs {
   int32_t w_f32;     // the weight is float32 (else of x's type)
   int32_t e5m2;
 };
-// vec: rows in 16-byte units (every leading dimension and pointer fits), else element by element
-hipError_t launch_norm_forward(const NormArgs& a, mr_dtype dt, bool vec, hipStream_t s);
+hipError_t launch_norm_forward(const NormArgs& a, mr_dtype dt, hipStream_t s);
 // `blocks` workgroups (norm_backward_blocks), their column sums in a.partial
-hipError_t launch_norm_backward(const NormArgs& a, mr_dtype dt, bool vec, int blocks, hipStream_t s);
+hipError_t launch_norm_backward(const NormArgs& a, mr_dtype dt, int blocks, hipStream_t s);
 hipError_t launch_norm_weight_grad(const float* partial, int blocks, int width, float* dweight, hipStream_t s);
 int norm_backward_blocks(int64_t rows, int64_t width);
 
@@ -50,9 +49,8 @@ struct QuantArgs {
   int64_t m;
   int32_t n;
   int32_t square, e5m2;
-  int32_t vec_q, vec_qt;  // 8-byte rows of q, 16-byte rows of qt
 };
-hipError_t launch_quantize(const QuantArgs& a, mr_dtype dt, bool vec, hipStream_t s);
+hipError_t launch_quantize(const QuantArgs& a, mr_dtype dt, hipStream_t s);
 
 // C (m x n) = A B^T with block scales.  In the kernels "P" is the operand on
 // the matrix instruction's rows (B: a lane holds four consecutive columns of

@@ -11,6 +11,11 @@ namespace mr {
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+// The same at any address: one load or store instruction all the same (the
+// hardware takes unaligned vector accesses), so rows of odd widths move like
+// the others.
+typedef v4u v4u_any __attribute__((aligned(1)));
+typedef v2u v2u_any __attribute__((aligned(1)));
 
 struct bf16_t {
   uint16_t bits;
@@ -38,7 +43,7 @@ __device__ __forceinline__ bf16_t narrow<bf16_t>(float v) {
   return r;
 }
 
-// Eight consecutive values as they are stored: one 16-byte unit (two for float32).
+// Eight consecutive values as they are stored, at any address: 16 bytes (twice that for float32).
 template <typename T>
 struct Raw8 {
   v4u u[sizeof(T) / 2];
@@ -47,7 +52,7 @@ template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p) {
   Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const v4u*>(p)[i];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const v4u_any*>(p)[i];
   return r;
 }
 __device__ __forceinline__ void widen8(const Raw8<float>& r, float (&v)[8]) {
@@ -75,7 +80,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   Raw8<T> r;
   __builtin_memcpy(&r, t, sizeof r);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<v4u*>(p)[i] = r.u[i];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<v4u_any*>(p)[i] = r.u[i];
 }
 
 // Four values in 8 bits (ties to even; the callers' scale keeps them in range).

@@ -407,8 +407,8 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
     const int64_t k0 = (int64_t)c * kChunkBytes;
     const int left = (int)min((int64_t)kChunkBytes, a.k - k0);
     __syncthreads();
-    edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, t.p0, t.pv, k0, left, false, lds, threadIdx.x);
-    edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, t.q0, t.qv, k0, left, false, lds + S::P_BYTES, threadIdx.x);
+    edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, t.p0, t.pv, k0, left, lds, threadIdx.x);
+    edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, t.q0, t.qv, k0, left, lds + S::P_BYTES, threadIdx.x);
     __syncthreads();
     typename Frag8<WIDE, QF>::type fq[S::CB];
     float sc[S::CB];
@@ -467,7 +467,7 @@ __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a
     const int left = a.k - (int)k0;
     if (a.fast && c * kChunkBytes + kChunkBytes <= a.k)
       return join(*reinterpret_cast<const v4i*>(row + k0), *reinterpret_cast<const v4i*>(row + k0 + 64));
-    const v4u u = edge_unit<1>(row + k0, left, a.fast), v = edge_unit<1>(row + k0 + 64, left - 64, a.fast);
+    const v4u u = edge_unit<1>(row + k0, left), v = edge_unit<1>(row + k0 + 64, left - 64);
     return join(__builtin_bit_cast(v4i, u), __builtin_bit_cast(v4i, v));
   };
   for (int c = wave; c < chunks; c += NW) {

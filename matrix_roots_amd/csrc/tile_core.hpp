@@ -74,11 +74,12 @@ __device__ __forceinline__ void copy_across(const unsigned char* base, int64_t l
   }
 }
 
-// 16 bytes at p of which the first `n` (elements of ES bytes) exist; zeros after.
+// 16 bytes at p (any address) of which the first `n` (elements of ES bytes)
+// exist; zeros after.
 template <int ES>
-__device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n, bool aligned) {
+__device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n) {
   v4u r = {0, 0, 0, 0};
-  if (n >= 16 / ES && aligned) return *reinterpret_cast<const v4u*>(p);
+  if (n >= 16 / ES) return *reinterpret_cast<const v4u_any*>(p);
 #pragma unroll
   for (int i = 0; i < 16 / ES; ++i)
     if (i < n) {
@@ -94,24 +95,24 @@ __device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n, bool ali
 // reaches the sums.
 template <int R, int THREADS, int ES, int UPR>
 __device__ __forceinline__ void edge_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
-                                           int k_left, bool aligned, unsigned char* stage, int thread) {
+                                           int k_left, unsigned char* stage, int thread) {
 #pragma unroll 1
   for (int u = thread; u < R * UPR; u += THREADS) {
     const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
-    if (row < valid) v = edge_unit<ES>(base + (row0 + row) * ld_bytes + k0 + unit * 16, k_left - unit * (16 / ES), aligned);
+    if (row < valid) v = edge_unit<ES>(base + (row0 + row) * ld_bytes + k0 + unit * 16, k_left - unit * (16 / ES));
     *reinterpret_cast<v4u*>(stage + (row * UPR + dl_slot(row, unit, UPR)) * 16) = v;
   }
 }
 template <int R, int THREADS, int BK>
 __device__ __forceinline__ void edge_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int k_left, int64_t col0,
-                                            int valid, bool aligned, unsigned char* stage, int thread) {
+                                            int valid, unsigned char* stage, int thread) {
   constexpr int UPR = R / 8;
 #pragma unroll 1
   for (int u = thread; u < BK * UPR; u += THREADS) {
     const int row = u / UPR, unit = u % UPR;
     v4u v = {0, 0, 0, 0};
-    if (row < k_left) v = edge_unit<2>(base + (k0 + row) * ld_bytes + (col0 + unit * 8) * 2, valid - unit * 8, aligned);
+    if (row < k_left) v = edge_unit<2>(base + (k0 + row) * ld_bytes + (col0 + unit * 8) * 2, valid - unit * 8);
     *reinterpret_cast<v4u*>(stage + (row * UPR + (unit ^ across_swap<R>(row))) * 16) = v;
   }
 }

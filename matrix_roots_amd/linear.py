@@ -41,30 +41,42 @@ class Quantized(NamedTuple):
     scales_t: Optional[torch.Tensor]
 
 
-def _device(*tensors):
+def _device(first, *others):
     """The one GPU the tensors are on, which has to be torch's current one."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one GPU")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, not on the current device")
-    return dev
+    if index < 0:
+        raise ValueError("all tensors must be on one GPU")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on GPU {index}, not on the current one")
+    return first.device
+
+
+# The current stream's handle without a Stream object around it (2 us of a 10 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, dev) -> int:
-    return int((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return _raw_stream(dev.index) if _raw_stream is not None else int(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _ld(t) -> int:
     """Leading dimension in elements (any that fits, where there is one row at most)."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2:
         raise ValueError("matrices must be 2-D with unit column stride")
-    return int(t.stride(0)) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError("matrices must be 2-D with unit column stride")
+    return ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _same_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
@@ -191,9 +203,9 @@ def _scales(name, s, rows, k):
     """(block code, leading dimension) of a scale matrix for `rows` rows."""
     if s.dtype != torch.float32:
         raise ValueError(f"{name} must be float32")
-    if s.dim() == 2 and tuple(s.shape) == (rows, _blocks(k)):
+    if s.shape == (rows, _blocks(k)):
         return B.MR_BLOCK_VECTOR, _ld(s)
-    _same_shape(name, s, (_blocks(rows), _blocks(k)))
+    _same_shape(name, s, torch.Size((_blocks(rows), _blocks(k))))
     return B.MR_BLOCK_SQUARE, _ld(s)
 
 
