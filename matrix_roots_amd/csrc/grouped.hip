@@ -15,6 +15,8 @@
 // tiles (rows / tile + experts); every workgroup finds its own from the
 // offsets (one wave scan per 64 experts), so no size reaches the host and the
 // call can be captured and replayed under other sizes.
+#include <type_traits>
+
 #include "tile_core.hpp"
 
 namespace mr {
@@ -119,6 +121,49 @@ struct RowTiles {
   }
 };
 
+// The weights' gradients' tiles, `tiles` to an expert, shared out to the XCDs by
+// what they cost: an expert's tile takes its chunks of BK rows and, for its
+// stores, what kStoreChunks chunks take.  Contiguous runs of equal cost keep an
+// expert's operands in one or two L2s (runs of equal length: 300 us with uneven
+// experts where even ones took 214).
+constexpr int kStoreChunks = 5;
+template <int BK>
+__device__ __forceinline__ Walk share_experts(const GroupedArgs& a, int tiles) {
+  const int lane = threadIdx.x & 63, per = (a.experts + 63) / 64;
+  auto cost = [&](int e) -> int64_t {
+    if (e >= a.experts) return 0;
+    int64_t b, t;
+    expert_rows(a, e, b, t);
+    return (t - b + BK - 1) / BK + kStoreChunks;
+  };
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) mine += cost(lane * per + i);
+  int64_t sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t up = __shfl_up(sum, d);
+    if (lane >= d) sum += up;
+  }
+  const int64_t total = __shfl(sum, 63);
+  // first tile of XCD x: the tiles before it cost x / 8 of all
+  auto first = [&](int x) {
+    if (x >= kNumXcd) return a.experts * tiles;
+    int64_t left = total * tiles * x / kNumXcd;  // (in units of one tile's cost)
+    const uint64_t hit = __ballot(left < sum * tiles);
+    const int l = hit ? __builtin_ctzll(hit) : 63;
+    left -= (__shfl(sum, l) - __shfl(mine, l)) * tiles;
+    int e = l * per;
+    for (int i = 1; i < per && left >= cost(e) * tiles; ++i) {
+      left -= cost(e) * tiles;
+      ++e;
+    }
+    e = min(e, a.experts - 1);
+    return e * tiles + (int)min(left / max(cost(e), (int64_t)1), (int64_t)tiles);
+  };
+  const int x = blockIdx.x % kNumXcd;
+  return Walk(first(x), first(x + 1));
+}
+
 }  // namespace
 
 // WP x WQ waves multiply, kLoaders waves copy.  NST stages of BK steps in LDS;
@@ -143,23 +188,25 @@ struct Operand {
   int valid;
 };
 
-// One operand's part of a chunk, by the loader waves.
+// One operand's part of a chunk by direct copies of the loader waves.
 template <class S, int R, bool ACROSS>
-__device__ __forceinline__ void stage_operand(const Operand& o, bool direct, int64_t k0, int left,
-                                              unsigned char* st, int loader, int lane) {
-  const int thread = loader * 64 + lane;
-  if constexpr (ACROSS) {
-    if (direct)
-      copy_across<R, kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, loader, lane);
-    else
-      edge_across<R, 64 * kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, thread);
-  } else {
-    if (direct)
-      copy_along<R, kLoaders, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, (left + 7) / 8, st, loader, lane);
-    else
-      edge_along<R, 64 * kLoaders, 2, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, left, st, thread);
-  }
+__device__ __forceinline__ void copy_operand(const Operand& o, int64_t k0, int left, unsigned char* st, int loader, int lane) {
+  if constexpr (ACROSS)
+    copy_across<R, kLoaders, S::BK>(o.base, o.ld_bytes, k0, left, o.r0, o.valid, st, loader, lane);
+  else
+    copy_along<R, kLoaders, S::BK / 8>(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, (left + 7) / 8, st, loader, lane);
 }
+// ... and through their registers.
+template <class S, int R, bool ACROSS>
+struct EdgeOperand {
+  std::conditional_t<ACROSS, EdgeAcross<R, 64 * kLoaders, S::BK>, EdgeAlong<R, 64 * kLoaders, 2, S::BK / 8>> e;
+  __device__ __forceinline__ void load(const Operand& o, int64_t k0, int left, int thread) {
+    if constexpr (ACROSS)
+      e.load(o.base, o.ld_bytes, k0, left, o.r0, o.valid, thread);
+    else
+      e.load(o.base, o.ld_bytes, o.r0, o.valid, k0 * 2, left, thread);
+  }
+};
 
 template <class S>
 struct Frags {
@@ -203,41 +250,65 @@ struct Tile {
   Operand P, Q;
   int64_t steps;
   int chunks;
-  bool direct;  // every chunk by whole 16-byte units
   int e, p0, pv, qv;
   int64_t q0;
-  template <bool PA, bool QA>
-  __device__ __forceinline__ void ready(int64_t n, bool fast) {
+  __device__ __forceinline__ void ready(int64_t n) {
     steps = n;
     chunks = (int)((n + S::BK - 1) / S::BK);
-    // a ragged edge that splits a unit goes element by element
-    const bool whole_p = PA ? (P.valid == S::BP || P.valid % 8 == 0) : n % 8 == 0;
-    const bool whole_q = QA ? (Q.valid == S::BQ || Q.valid % 8 == 0) : n % 8 == 0;
-    direct = fast && whole_p && whole_q;
   }
 };
 
-// The loader waves' side of stream_tiles.
-template <class S, bool PA, bool QA, class Load>
+// The loader waves' side of stream_tiles.  FAST: every operand by whole 16-byte
+// units at 16-byte addresses; else through registers, one chunk's loads ahead.
+template <class S, bool PA, bool QA, bool FAST, class Load>
 __device__ __forceinline__ void copy_stream(Walk w, unsigned char* lds, Load&& load, int loader, int lane) {
   Tile<S> t;
   t.chunks = 0;
   int c = 0;  // next chunk of t
-  copy_chunks<S::NST, S::COPIES>([&](int j) {
+  auto more = [&] {
     while (c == t.chunks) {
-      if (w.at >= w.end) return -1;
+      if (w.at >= w.end) return false;
       load(t, w.at);
       w.at += w.step;
       c = 0;
     }
-    unsigned char* st = lds + j % S::NST * S::STAGE;
-    const int64_t k0 = (int64_t)c * S::BK;
-    const int left = (int)min((int64_t)S::BK, t.steps - k0);
-    stage_operand<S, S::BP, PA>(t.P, t.direct, k0, left, st, loader, lane);
-    stage_operand<S, S::BQ, QA>(t.Q, t.direct, k0, left, st + S::P_BYTES, loader, lane);
-    ++c;
-    return t.direct ? 1 : 0;
-  });
+    return true;
+  };
+  if constexpr (FAST) {
+    copy_chunks<S::NST, true, S::COPIES>([&](int j) {
+      if (!more()) return false;
+      unsigned char* st = lds + j % S::NST * S::STAGE;
+      const int64_t k0 = (int64_t)c * S::BK;
+      const int left = (int)min((int64_t)S::BK, t.steps - k0);
+      copy_operand<S, S::BP, PA>(t.P, k0, left, st, loader, lane);
+      copy_operand<S, S::BQ, QA>(t.Q, k0, left, st + S::P_BYTES, loader, lane);
+      ++c;
+      return true;
+    });
+  } else {
+    const int thread = loader * 64 + lane;
+    EdgeOperand<S, S::BP, PA> p;
+    EdgeOperand<S, S::BQ, QA> q;
+    bool held = false;
+    auto fetch = [&] {
+      held = more();
+      if (!held) return;
+      const int64_t k0 = (int64_t)c * S::BK;
+      const int left = (int)min((int64_t)S::BK, t.steps - k0);
+      p.load(t.P, k0, left, thread);
+      q.load(t.Q, k0, left, thread);
+      ++c;
+    };
+    fetch();
+    copy_chunks<S::NST, false, 0>([&](int j) {
+      if (!held) return false;
+      unsigned char* st = lds + j % S::NST * S::STAGE;
+      p.e.store(st, thread);
+      q.e.store(st + S::P_BYTES, thread);
+      fetch();
+      return true;
+    });
+  }
 }
 
 // A workgroup's tiles, one after another, as one stream of chunks through NST
@@ -248,12 +319,12 @@ __device__ __forceinline__ void copy_stream(Walk w, unsigned char* lds, Load&& l
 // step of products, whose fragments are in registers by then; one more at the
 // end of the stream.  load(tile, id) describes tile `id`, put(tile, acc, slab)
 // stores one.
-template <class S, typename T, bool PA, bool QA, class Load, class Put>
+template <class S, typename T, bool PA, bool QA, bool FAST, class Load, class Put>
 __device__ __forceinline__ void stream_tiles(Walk w, unsigned char* lds, Load&& load, Put&& put) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= S::NW) {
-    copy_stream<S, PA, QA>(w, lds, load, wave - S::NW, lane);
+    copy_stream<S, PA, QA, FAST>(w, lds, load, wave - S::NW, lane);
     return;
   }
   const int wp = wave / S::WQ, wq = wave % S::WQ;
@@ -383,7 +454,7 @@ __device__ __forceinline__ void put_weight(const GroupedArgs& a, O* w, int p0, i
     }
 }
 
-template <class S, typename T, bool TRANSPOSE>
+template <class S, typename T, bool TRANSPOSE, bool FAST>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_kernel(const GroupedArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
   const int outs = TRANSPOSE ? a.k : a.n, steps = TRANSPOSE ? a.n : a.k;
@@ -402,7 +473,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_ke
     t.qv = (int)min((int64_t)S::BQ, end - t.q0);
     t.P = Operand{reinterpret_cast<const unsigned char*>(a.w) + t.e * a.w_stride * 2, a.ldw * 2, t.p0, t.pv};
     t.Q = Operand{reinterpret_cast<const unsigned char*>(a.x), a.ldx * 2, t.q0, t.qv};
-    t.template ready<TRANSPOSE, false>(t.qv > 0 ? steps : 0, a.fast);
+    t.ready(t.qv > 0 ? steps : 0);
   };
   auto put = [&](const Tile<S>& t, const v16f(&acc)[S::RB][S::CB], unsigned char* slab) {
     if (a.y_f32)
@@ -410,7 +481,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_ke
     else
       put_rows<S, T>(a, t.q0, t.qv, t.p0, t.pv, slab, acc);
   };
-  stream_tiles<S, T, TRANSPOSE, false>(Walk(tiles.total), lds, load, put);
+  stream_tiles<S, T, TRANSPOSE, false, FAST>(Walk(tiles.total), lds, load, put);
   // rows of no expert: before the first and after the last offset
   const int64_t first = offset_at(a, 0), last = max(offset_at(a, a.experts), first);
   const int es = a.y_f32 ? 4 : 2;
@@ -425,7 +496,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_ke
   }
 }
 
-template <class S, typename T>
+template <class S, typename T, bool FAST>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_kernel(const GroupedArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
   const int tp = (a.n + S::BP - 1) / S::BP, tq = (a.k + S::BQ - 1) / S::BQ;
@@ -440,7 +511,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_
     t.qv = min(S::BQ, a.k - (int)t.q0);
     t.P = Operand{reinterpret_cast<const unsigned char*>(a.x) + begin * a.ldx * 2, a.ldx * 2, t.p0, t.pv};
     t.Q = Operand{reinterpret_cast<const unsigned char*>(a.w) + begin * a.ldw * 2, a.ldw * 2, t.q0, t.qv};
-    t.template ready<true, true>(end - begin, a.fast);
+    t.ready(end - begin);
   };
   auto put = [&](const Tile<S>& t, const v16f(&acc)[S::RB][S::CB], unsigned char*) {
     if (a.y_f32)
@@ -448,16 +519,17 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_
     else
       put_weight<S>(a, reinterpret_cast<T*>(a.y) + t.e * a.y_stride, t.p0, t.pv, (int)t.q0, t.qv, acc);
   };
-  stream_tiles<S, T, true, true>(Walk(a.experts * tp * tq), lds, load, put);
+  stream_tiles<S, T, true, true, FAST>(share_experts<S::BK>(a, tp * tq), lds, load, put);
 }
 
 // ------------------------------------------------------------ launchers
 namespace {
 
-using RowsWide = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
-using RowsNarrow = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
-using RowsFew = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
-using Weights = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
+using Large = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
+using Middle = GroupedShape<128, 64, 2, 2, 64, 4, 1>;
+using Small = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
+using MiddleWeights = GroupedShape<128, 64, 2, 2, 64, 4, 1>;
+using Edge = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
 
 template <class K>
 hipError_t raise_lds(K kernel, int bytes, bool& raised) {
@@ -467,10 +539,10 @@ hipError_t raise_lds(K kernel, int bytes, bool& raised) {
   return e;
 }
 
-template <class S, typename T, bool TRANSPOSE>
+template <class S, typename T, bool TRANSPOSE, bool FAST>
 hipError_t go_rows(const GroupedArgs& a, hipStream_t s) {
   static bool raised = false;
-  auto kernel = grouped_tile_kernel<S, T, TRANSPOSE>;
+  auto kernel = grouped_tile_kernel<S, T, TRANSPOSE, FAST>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t outs = TRANSPOSE ? a.k : a.n;
   const int64_t groups = a.experts < a.rows ? a.experts : a.rows;
@@ -479,22 +551,43 @@ hipError_t go_rows(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class S, typename T>
+template <class S, typename T, bool FAST>
 hipError_t go_weights(const GroupedArgs& a, hipStream_t s) {
   static bool raised = false;
-  auto kernel = grouped_weight_kernel<S, T>;
+  auto kernel = grouped_weight_kernel<S, T, FAST>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t tiles = (int64_t)a.experts * ((a.n + S::BP - 1) / S::BP) * ((a.k + S::BQ - 1) / S::BQ);
   hipLaunchKernelGGL(kernel, dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
 }
 
+// Rounds of tiles that the CUs go through, times what a chunk of such a tile
+// takes (in tenths of a microsecond, measured).
+template <class S>
+int64_t cost(int64_t tiles, int chunk) {
+  const int64_t slots = 256 * S::BPC;
+  return (tiles + slots - 1) / slots * chunk;
+}
+
 template <typename T, bool TRANSPOSE>
 hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
-  const int outs = TRANSPOSE ? a.k : a.n;
-  if (a.rows <= 32 * (int64_t)a.experts) return go_rows<RowsFew, T, TRANSPOSE>(a, s);
-  if (outs > 128) return go_rows<RowsWide, T, TRANSPOSE>(a, s);
-  return go_rows<RowsNarrow, T, TRANSPOSE>(a, s);
+  const int64_t outs = TRANSPOSE ? a.k : a.n;
+  // experts of equal size, as many as can have rows
+  const int64_t groups = a.experts < a.rows ? a.experts : a.rows, each = (a.rows + groups - 1) / groups;
+  auto tiles = [&](int p, int q) { return groups * ((each + q - 1) / q) * ((outs + p - 1) / p); };
+  if (!a.fast) return go_rows<Edge, T, TRANSPOSE, false>(a, s);
+  const int64_t l = cost<Large>(tiles(256, 128), 10), m = cost<Middle>(tiles(128, 64), 7), n = cost<Small>(tiles(64, 32), 8);
+  if (n < l && n < m) return go_rows<Small, T, TRANSPOSE, true>(a, s);
+  if (m < l) return go_rows<Middle, T, TRANSPOSE, true>(a, s);
+  return go_rows<Large, T, TRANSPOSE, true>(a, s);
+}
+
+template <typename T>
+hipError_t pick_weights(const GroupedArgs& a, hipStream_t s) {
+  auto tiles = [&](int p, int q) { return (int64_t)a.experts * ((a.n + p - 1) / p) * ((a.k + q - 1) / q); };
+  if (!a.fast) return go_weights<Edge, T, false>(a, s);
+  const int64_t l = cost<Large>(tiles(256, 128), 10), m = cost<MiddleWeights>(tiles(128, 64), 7);
+  return m < l ? go_weights<MiddleWeights, T, true>(a, s) : go_weights<Large, T, true>(a, s);
 }
 
 }  // namespace
@@ -505,7 +598,7 @@ hipError_t launch_grouped(const GroupedArgs& a, mr_dtype dt, bool transpose, hip
 }
 
 hipError_t launch_grouped_weight_grad(const GroupedArgs& a, mr_dtype dt, hipStream_t s) {
-  return dt == MR_F16 ? go_weights<Weights, _Float16>(a, s) : go_weights<Weights, bf16_t>(a, s);
+  return dt == MR_F16 ? pick_weights<_Float16>(a, s) : pick_weights<bf16_t>(a, s);
 }
 
 }  // namespace mr

@@ -322,7 +322,8 @@ mr_status grouped_matmul(const mr_grouped_problem* p, void* hip_stream) {
   a.y = p->Y, a.ldy = p->ldy;
   a.offsets = p->offsets, a.wide_offsets = p->offset_bits == 64;
   a.rows = p->rows, a.experts = (int32_t)p->experts, a.n = (int32_t)p->n, a.k = (int32_t)p->k;
-  a.fast = units16(p->X, p->ldx, 2) && units16(p->W, p->ldw, 2) && (p->w_stride % 8 == 0 || p->experts == 1);
+  a.fast = units16(p->X, p->ldx, 2) && units16(p->W, p->ldw, 2) && (p->w_stride % 8 == 0 || p->experts == 1) &&
+           p->k % 8 == 0 && (!p->transpose || p->n % 8 == 0);
   a.vec_y = units16(p->Y, p->ldy, ys);
   a.y_f32 = p->y_dtype == MR_F32;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
@@ -354,7 +355,7 @@ mr_status grouped_weight_grad(const mr_grouped_grad_problem* p, void* hip_stream
   a.y = p->DW, a.ldy = p->lddw, a.y_stride = p->dw_stride;
   a.offsets = p->offsets, a.wide_offsets = p->offset_bits == 64;
   a.rows = p->rows, a.experts = (int32_t)p->experts, a.n = (int32_t)p->n, a.k = (int32_t)p->k;
-  a.fast = units16(p->DY, p->lddy, 2) && units16(p->X, p->ldx, 2);
+  a.fast = units16(p->DY, p->lddy, 2) && units16(p->X, p->ldx, 2) && p->n % 8 == 0 && p->k % 8 == 0;
   a.y_f32 = p->dw_dtype == MR_F32;
   a.accumulate = p->accumulate != 0;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);

@@ -68,7 +68,7 @@ struct ScaledArgs {
   int32_t p_vector;        // P's scales: one per row (else per 128 rows)
   int32_t p_shift;         // P's scales: row >> p_shift (0: one per row, 7: per 128 rows)
   int32_t q_shift;         // Q's scales: row >> q_shift (0: one per row, 7: per 128 rows)
-  int32_t fast;            // rows of both operands in 16-byte units
+  int32_t fast;            // both operands in whole 16-byte units at 16-byte addresses
   int32_t q_e5m2;
   int32_t c_type;          // mr_dtype
   int32_t accumulate;
@@ -93,7 +93,7 @@ struct GroupedArgs {
   int64_t rows;
   int32_t experts, n, k;
   int32_t wide_offsets;  // 64-bit offsets
-  int32_t fast;          // operand rows in 16-byte units
+  int32_t fast;          // operands in whole 16-byte units at 16-byte addresses
   int32_t vec_y;
   int32_t y_f32;
   int32_t accumulate;

@@ -407,8 +407,12 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
     const int64_t k0 = (int64_t)c * kChunkBytes;
     const int left = (int)min((int64_t)kChunkBytes, a.k - k0);
     __syncthreads();
-    edge_along<S::BP, S::THREADS, 1, 8>(a.p, a.ldp, t.p0, t.pv, k0, left, lds, threadIdx.x);
-    edge_along<S::BQ, S::THREADS, 1, 8>(a.q, a.ldq, t.q0, t.qv, k0, left, lds + S::P_BYTES, threadIdx.x);
+    EdgeAlong<S::BP, S::THREADS, 1, 8> ep;
+    EdgeAlong<S::BQ, S::THREADS, 1, 8> eq;
+    ep.load(a.p, a.ldp, t.p0, t.pv, k0, left, threadIdx.x);
+    eq.load(a.q, a.ldq, t.q0, t.qv, k0, left, threadIdx.x);
+    ep.store(lds, threadIdx.x);
+    eq.store(lds + S::P_BYTES, threadIdx.x);
     __syncthreads();
     typename Frag8<WIDE, QF>::type fq[S::CB];
     float sc[S::CB];
@@ -559,7 +563,11 @@ hipError_t go_edge(const ScaledArgs& a, hipStream_t s) {
 template <int CB, int QF, bool PVEC, bool WIDE>
 hipError_t go_rows(const ScaledArgs& a, hipStream_t s) {
   const dim3 grid((a.n + 15) / 16);
-  hipLaunchKernelGGL((scaled_rows_kernel<CB, 8, QF, PVEC, WIDE>), grid, dim3(512), 0, s, a);
+  // long contractions under few columns: twice the waves, for bytes in flight
+  if (CB == 1 && grid.x < kCus && a.k >= 32 * kChunkBytes)
+    hipLaunchKernelGGL((scaled_rows_kernel<CB, CB == 1 ? 16 : 8, QF, PVEC, WIDE>), grid, dim3(CB == 1 ? 1024 : 512), 0, s, a);
+  else
+    hipLaunchKernelGGL((scaled_rows_kernel<CB, 8, QF, PVEC, WIDE>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

@@ -89,33 +89,68 @@ __device__ __forceinline__ v4u edge_unit(const unsigned char* p, int n) {
   return r;
 }
 
-// The same chunks by the THREADS threads from `thread` on with every element
-// checked: rows past `valid` and contraction
-// steps past k_left are zeros, so that nothing that lies there (not even a NaN)
-// reaches the sums.
+// The same chunks by THREADS threads through registers, for rows at any address
+// and ragged ends, in two halves (the loads of one chunk can run ahead of its
+// stores): rows past `valid` and contraction steps past k_left become zeros, so
+// that nothing that lies there (not even a NaN) reaches the sums.
 template <int R, int THREADS, int ES, int UPR>
-__device__ __forceinline__ void edge_along(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
-                                           int k_left, unsigned char* stage, int thread) {
-#pragma unroll 1
-  for (int u = thread; u < R * UPR; u += THREADS) {
-    const int row = u / UPR, unit = u % UPR;
-    v4u v = {0, 0, 0, 0};
-    if (row < valid) v = edge_unit<ES>(base + (row0 + row) * ld_bytes + k0 + unit * 16, k_left - unit * (16 / ES));
-    *reinterpret_cast<v4u*>(stage + (row * UPR + dl_slot(row, unit, UPR)) * 16) = v;
+struct EdgeAlong {
+  static constexpr int N = (R * UPR + THREADS - 1) / THREADS, EU = 16 / ES;
+  v4u v[N];
+  __device__ __forceinline__ void load(const unsigned char* base, int64_t ld_bytes, int64_t row0, int valid, int64_t k0,
+                                       int k_left, int thread) {
+    const unsigned char* p = base + row0 * ld_bytes + k0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      v[j] = {0, 0, 0, 0};
+      if (u < R * UPR && row < valid && unit * EU + EU <= k_left)
+        v[j] = *reinterpret_cast<const v4u_any*>(p + row * ld_bytes + unit * 16);
+    }
+    if (k_left >= UPR * EU || k_left % EU == 0) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {  // the unit that the contraction ends in, element by element
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      if (u < R * UPR && row < valid && unit == k_left / EU) v[j] = edge_unit<ES>(p + row * ld_bytes + unit * 16, k_left % EU);
+    }
   }
-}
+  __device__ __forceinline__ void store(unsigned char* stage, int thread) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      if (u < R * UPR) *reinterpret_cast<v4u*>(stage + (row * UPR + dl_slot(row, unit, UPR)) * 16) = v[j];
+    }
+  }
+};
 template <int R, int THREADS, int BK>
-__device__ __forceinline__ void edge_across(const unsigned char* base, int64_t ld_bytes, int64_t k0, int k_left, int64_t col0,
-                                            int valid, unsigned char* stage, int thread) {
-  constexpr int UPR = R / 8;
-#pragma unroll 1
-  for (int u = thread; u < BK * UPR; u += THREADS) {
-    const int row = u / UPR, unit = u % UPR;
-    v4u v = {0, 0, 0, 0};
-    if (row < k_left) v = edge_unit<2>(base + (k0 + row) * ld_bytes + (col0 + unit * 8) * 2, valid - unit * 8);
-    *reinterpret_cast<v4u*>(stage + (row * UPR + (unit ^ across_swap<R>(row))) * 16) = v;
+struct EdgeAcross {
+  static constexpr int UPR = R / 8, N = (BK * UPR + THREADS - 1) / THREADS;
+  v4u v[N];
+  __device__ __forceinline__ void load(const unsigned char* base, int64_t ld_bytes, int64_t k0, int k_left, int64_t col0,
+                                       int valid, int thread) {
+    const unsigned char* p = base + k0 * ld_bytes + col0 * 2;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      v[j] = {0, 0, 0, 0};
+      if (u < BK * UPR && row < k_left && unit * 8 + 8 <= valid)
+        v[j] = *reinterpret_cast<const v4u_any*>(p + row * ld_bytes + unit * 16);
+    }
+    if (valid >= R || valid % 8 == 0) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      if (u < BK * UPR && row < k_left && unit == valid / 8) v[j] = edge_unit<2>(p + row * ld_bytes + unit * 16, valid % 8);
+    }
   }
-}
+  __device__ __forceinline__ void store(unsigned char* stage, int thread) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int u = thread + j * THREADS, row = u / UPR, unit = u % UPR;
+      if (u < BK * UPR) *reinterpret_cast<v4u*>(stage + (row * UPR + (unit ^ across_swap<R>(row))) * 16) = v[j];
+    }
+  }
+};
 
 // Four consecutive outputs of a row, `left` of them inside the matrix.
 template <typename T>
@@ -217,12 +252,12 @@ __device__ __forceinline__ void stage_barrier() {
 // the tiles in flight on an XCD are neighbours and share operands in its L2.
 struct Walk {
   int at, step, end;
-  __device__ __forceinline__ Walk(int total) {
-    const int x = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
-    end = (int)((int64_t)total * (x + 1) / kNumXcd);
-    at = (int)((int64_t)total * x / kNumXcd) + blockIdx.x / kNumXcd;
-    step = slots;
-  }
+  // tiles begin .. end of this XCD
+  __device__ __forceinline__ Walk(int begin, int end_)
+      : at(begin + blockIdx.x / kNumXcd), step(gridDim.x / kNumXcd), end(end_) {}
+  __device__ __forceinline__ explicit Walk(int total)
+      : Walk((int)((int64_t)total * (blockIdx.x % kNumXcd) / kNumXcd),
+             (int)((int64_t)total * (blockIdx.x % kNumXcd + 1) / kNumXcd)) {}
 };
 // Workgroups of a launch over at most `tiles` tiles: what the CUs hold at a
 // time, a multiple of the XCDs.
@@ -235,29 +270,29 @@ inline unsigned persistent_blocks(int64_t tiles, int per_cu) {
 // operands to LDS, the others multiply and store.
 constexpr int kLoaders = 4;
 
-// The loader waves' side of a stream of chunks through NST stages, COPIES direct
-// copies a wave and chunk.  issue(j) puts the stream's chunk j into stage j %
-// NST: 1 by direct copies only, 0 with LDS stores among them, -1 past the end.
-// One barrier per chunk: before it the loaders wait for that chunk's copies
-// alone, after it the stage of its predecessor is free.
-template <int NST, int COPIES, class Issue>
+// The loader waves' side of a stream of chunks through NST stages: issue(j) puts
+// the stream's chunk j into stage j % NST, false past the end.  With DIRECT by
+// COPIES direct copies a wave, else by LDS stores.  One barrier per chunk:
+// before it the loaders wait for that chunk alone, after it the stage of its
+// predecessor is free.
+template <int NST, bool DIRECT, int COPIES, class Issue>
 __device__ __forceinline__ void copy_chunks(Issue&& issue) {
   static_assert((NST - 2) * COPIES < 64, "the wait counts to 63");
-  int issued = 0, stored = -1;  // chunks issued, the last one with LDS stores
+  int issued = 0;
   auto next = [&] {
-    const int r = issue(issued);
-    if (r < 0) return false;
-    if (r == 0) stored = issued;
-    ++issued;
-    return true;
+    const bool r = issue(issued);
+    issued += r;
+    return r;
   };
   for (int i = 0; i < NST - 1; ++i) next();
   for (int j = 0;; ++j) {
-    // chunk j has landed once at most the copies of the NST - 2 after it are in flight
-    if (issued - 1 - j == NST - 2 && stored <= j)
-      wait_vmcnt<(NST - 2) * COPIES>();
-    else
-      wait_vmcnt<0>();
+    if constexpr (DIRECT) {
+      // chunk j has landed once at most the copies of the NST - 2 after it are in flight
+      if (issued - 1 - j == NST - 2)
+        wait_vmcnt<(NST - 2) * COPIES>();
+      else
+        wait_vmcnt<0>();
+    }
     wait_lgkmcnt0();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();  // chunk j is in LDS; every wave is done with chunk j - 1
