@@ -116,7 +116,6 @@ struct ScaledShape {
   static constexpr int SP = P_BYTES + Q_BYTES, SQ = SP + BP * 4, STAGE = SQ + BQ * 4;
   static constexpr int NP = along_copies<BP, NW, 8>, NQ = along_copies<BQ, NW, 8>;  // copies per wave and chunk
   static constexpr int NS = (BP + BQ + 64 * NW - 1) / (64 * NW);
-  static constexpr int COPIES = NP + NQ + NS;
   static constexpr int SLABS = 2 * STAGE, LDS = SLABS + NW * Slab<float, 16>::BYTES;
   static constexpr int WAVES_PER_SIMD = BPC * NW / 4;
   static_assert(RB % 2 == 0 && BPC * LDS <= 160 * 1024, "the stages fit");
@@ -143,39 +142,64 @@ struct ScaledTile {
 };
 
 // The chunks of a workgroup's tiles in order, for the copies (past the last one
-// it stays on that one).
+// it stays on that one).  Scalar addresses move along with the chunks; a whole
+// tile's copies then cost a scalar addition each (worked out per chunk and copy,
+// the addresses took 20 us of 300 at 16384 x 8192 x 2048).
 template <class S>
 struct ScaledFeed {
   ScaledTile<S> t;
   Walk w;
-  int c, units, left;
+  int c, left;
+  bool whole;  // the tile has all its rows
   unsigned char* st;
   const char *p, *q, *sp, *sq;
-  __device__ __forceinline__ ScaledFeed(const ScaledArgs& a, const Walk& w_) : w(w_) {
+  uint32_t p_off, q_off;  // a lane's place in 8 NW rows of P, of Q
+  __device__ __forceinline__ ScaledFeed(const ScaledArgs& a, const Walk& w_, int wave, int lane) : w(w_) {
+    const int row = wave * 8 + (lane >> 3);
+    static_assert(8 * S::NW % 16 == 0, "the slot of a unit is the same in every group of rows");
+    const uint32_t slot = (uint32_t)dl_slot(row, lane & 7, 8) * 16u;
+    p_off = (uint32_t)row * (uint32_t)a.ldp + slot;
+    q_off = (uint32_t)row * (uint32_t)a.ldq + slot;
+    enter(a);
+  }
+  __device__ __forceinline__ void enter(const ScaledArgs& a) {  // the tile at w.at
     t.load(a, w.at);
     c = t.c_begin;
-  }
-  // The current chunk goes to `stage`.
-  __device__ __forceinline__ void begin(const ScaledArgs& a, unsigned char* stage) {
-    st = stage;
+    whole = t.pv == S::BP && t.qv == S::BQ;
     const int64_t k0 = (int64_t)c * kChunkBytes;
     left = (int)min((int64_t)kChunkBytes, a.k - k0);
-    units = (left + 15) >> 4;
     p = wave_uniform(a.p + (int64_t)t.p0 * a.ldp + k0);
     q = wave_uniform(a.q + t.q0 * a.ldq + k0);
     sp = wave_uniform(a.sp + (int64_t)(t.p0 >> a.p_shift) * a.ldsp + c);
     sq = wave_uniform(a.sq + (t.q0 >> a.q_shift) * a.ldsq + c);
   }
-  // Copy j (0 .. COPIES - 1) of the wave.
-  __device__ __forceinline__ void copy(const ScaledArgs& a, int j, int wave, int lane) {
-    if (j < S::NP) {
-      copy_along_one<S::BP, S::NW, 8>(p, a.ldp, t.pv, units, st, wave, lane, j);
-    } else if (j < S::NP + S::NQ) {
-      copy_along_one<S::BQ, S::NW, 8>(q, a.ldq, t.qv, units, st + S::P_BYTES, wave, lane, j - S::NP);
+  template <int N>
+  static __device__ __forceinline__ void copy_rows(const char* base, int64_t step, uint32_t off, unsigned char* to) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      asm volatile("" : "+v"(off));
+      __builtin_amdgcn_global_load_lds((global_void_ptr)(base + off), (lds_void_ptr)(to + j * S::NW * 1024), 16, 0, 0);
+      base += step;
+    }
+  }
+  // The wave's copies of the current chunk into `stage`.
+  __device__ __forceinline__ void copy(const ScaledArgs& a, unsigned char* stage, int wave, int lane) {
+    st = stage;
+    if (whole && left == kChunkBytes) {
+      copy_rows<S::NP>(p, (int64_t)(8 * S::NW) * a.ldp, p_off, st + wave * 1024);
+      copy_rows<S::NQ>(q, (int64_t)(8 * S::NW) * a.ldq, q_off, st + S::P_BYTES + wave * 1024);
     } else {
+      const int units = (left + 15) >> 4;
+#pragma unroll
+      for (int j = 0; j < S::NP; ++j) copy_along_one<S::BP, S::NW, 8>(p, a.ldp, t.pv, units, st, wave, lane, j);
+#pragma unroll
+      for (int j = 0; j < S::NQ; ++j) copy_along_one<S::BQ, S::NW, 8>(q, a.ldq, t.qv, units, st + S::P_BYTES, wave, lane, j);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NS; ++j) {
       // the scale of row i of P, then of Q, 64 rows to a copy (rows past the end repeat the last
       // one, surplus copies the first ones); tiles start at multiples of 128 rows
-      const int first = (((j - S::NP - S::NQ) * S::NW + wave) * 64) % (S::BP + S::BQ);
+      const int first = ((j * S::NW + wave) * 64) % (S::BP + S::BQ);
       const bool is_p = first < S::BP;
       const int row = min(is_p ? first + lane : first - S::BP + lane, (is_p ? t.pv : t.qv) - 1);
       uint32_t off = (uint32_t)(row >> (is_p ? a.p_shift : a.q_shift)) * (uint32_t)(is_p ? a.ldsp : a.ldsq) * 4u;
@@ -207,13 +231,16 @@ struct ScaledFeed {
     }
   }
   __device__ __forceinline__ void next(const ScaledArgs& a) {
-    if (++c < t.c_end) return;
-    if (w.at + w.step < w.end) {
+    if (c + 1 < t.c_end) {
+      ++c;
+      left = min(kChunkBytes, a.k - c * kChunkBytes);
+      p += kChunkBytes;
+      q += kChunkBytes;
+      sp += 4;
+      sq += 4;
+    } else if (w.at + w.step < w.end) {
       w.at += w.step;
-      t.load(a, w.at);
-      c = t.c_begin;
-    } else {
-      --c;
+      enter(a);
     }
   }
 };
@@ -284,7 +311,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
   auto read_sr = [&](const unsigned char* st, int rb) {
     if (PVEC) sr = *reinterpret_cast<const f4*>(st + S::SP + (prow + rb * 16 + 4 * (lane >> 4)) * 4);
   };
-  ScaledFeed<S> feed(a, w);
+  ScaledFeed<S> feed(a, w, wave, lane);
   auto land = [&] {  // the chunk being copied is in LDS; every wave has read the one before
     stage_barrier();
     if (feed.left < kChunkBytes) {
@@ -292,14 +319,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
       stage_barrier();
     }
   };
-  feed.begin(a, lds);
-#pragma unroll
-  for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+  feed.copy(a, lds, wave, lane);
   land();
   feed.next(a);
-  feed.begin(a, lds + S::STAGE);
-#pragma unroll
-  for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+  feed.copy(a, lds + S::STAGE, wave, lane);
 #pragma unroll
   for (int cb = 0; cb < S::CB; ++cb) fq[cb] = read_q(lds, cb);
   raw = frag8(lds, prow, lane);
@@ -340,9 +363,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
           raw = frag8(other, prow, lane);  // (past the stream's end: stale bytes that nothing uses)
           // this chunk's stage is free at once: the chunk after the next goes there
           feed.next(a);
-          feed.begin(a, st);
-#pragma unroll
-          for (int j = 0; j < S::COPIES; ++j) feed.copy(a, j, wave, lane);
+          feed.copy(a, st, wave, lane);
         } else {
           raw = frag8(st, prow + (rb + 1) * 16, lane);
         }
