@@ -191,15 +191,30 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_backward_kernel(const 
         dot = fmaf(g[k][i], hh[k][i], dot);
       }
     }
-    const float c = row_sum<TPR>(dot, red) * inv_width;
+    // under way during the reduction
     const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
+    Raw8<T> rr[CH];
+    if (res) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int col = chunk_col<TPR>(t, k);
+        if (col + 8 <= a.width) rr[k] = load8<T>(res + col);
+      }
+    }
+    const float c = row_sum<TPR>(dot, red) * inv_width;
     T* dx = reinterpret_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float u[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) u[i] = 0.f;
-      if (res) load_chunk<T>(res, chunk_col<TPR>(t, k), a.width, u);
+      if (res) {
+        const int col = chunk_col<TPR>(t, k);
+        if (col + 8 <= a.width)
+          widen8(rr[k], u);
+        else
+          load_chunk<T>(res, col, a.width, u);
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) u[i] += rho * (g[k][i] - hh[k][i] * c);
       store_chunk<T>(dx, chunk_col<TPR>(t, k), a.width, u);
@@ -227,12 +242,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_backward_kernel(const 
     if ((int)threadIdx.x >= TPR) return;
   }
 #pragma unroll
-  for (int k = 0; k < CH; ++k)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = chunk_col<TPR>(t, k) + i;
-      if (c < a.width) out[c] = dw[k][i];
-    }
+  for (int k = 0; k < CH; ++k) store_chunk<float>(out, chunk_col<TPR>(t, k), a.width, dw[k]);
 }
 
 // dweight[c] = sum over workgroups of their column sums: 32 columns per
