@@ -531,17 +531,9 @@ using Small = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
 using MiddleWeights = GroupedShape<128, 64, 2, 2, 64, 4, 1>;
 using Edge = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
 
-template <class K>
-hipError_t raise_lds(K kernel, int bytes, bool& raised) {
-  if (raised) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  raised = e == hipSuccess;
-  return e;
-}
-
 template <class S, typename T, bool TRANSPOSE, bool FAST>
 hipError_t go_rows(const GroupedArgs& a, hipStream_t s) {
-  static bool raised = false;
+  static std::atomic<uint64_t> raised{0};
   auto kernel = grouped_tile_kernel<S, T, TRANSPOSE, FAST>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t outs = TRANSPOSE ? a.k : a.n;
@@ -553,7 +545,7 @@ hipError_t go_rows(const GroupedArgs& a, hipStream_t s) {
 
 template <class S, typename T, bool FAST>
 hipError_t go_weights(const GroupedArgs& a, hipStream_t s) {
-  static bool raised = false;
+  static std::atomic<uint64_t> raised{0};
   auto kernel = grouped_weight_kernel<S, T, FAST>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t tiles = (int64_t)a.experts * ((a.n + S::BP - 1) / S::BP) * ((a.k + S::BQ - 1) / S::BQ);

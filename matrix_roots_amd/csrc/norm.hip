@@ -101,13 +101,14 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_forward_kernel(const N
     for (int k = 0; k < CH; ++k) load_chunk<T>(x, chunk_col<TPR>(t, k), a.width, v[k]);
     if (res) {
       T* h = reinterpret_cast<T*>(a.h) + r * a.ldh;
+      float u[CH][NV];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) load_chunk<T>(res, chunk_col<TPR>(t, k), a.width, u[k]);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float u[NV];
-        load_chunk<T>(res, chunk_col<TPR>(t, k), a.width, u);
         // the stored sum, rounded to T, is what the norm is of: the backward pass reads it
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[k][i] = widen(narrow<T>(v[k][i] + u[i]));
+        for (int i = 0; i < NV; ++i) v[k][i] = widen(narrow<T>(v[k][i] + u[k][i]));
         store_chunk<T>(h, chunk_col<TPR>(t, k), a.width, v[k]);
       }
     }

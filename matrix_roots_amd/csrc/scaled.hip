@@ -560,16 +560,11 @@ constexpr int kCus = 256;
 
 template <class S, int QF, bool PVEC, bool WIDE>
 hipError_t go_tile(const ScaledArgs& a, hipStream_t s) {
-  static bool raised = false;
-  if (!raised) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(scaled_tile_kernel<S, QF, PVEC, WIDE>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
-    if (e != hipSuccess) return e;
-    raised = true;
-  }
+  static std::atomic<uint64_t> raised{0};
+  auto kernel = scaled_tile_kernel<S, QF, PVEC, WIDE>;
+  if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t tiles = (int64_t)((a.n + S::BP - 1) / S::BP) * ((a.m + S::BQ - 1) / S::BQ) * a.splits;
-  hipLaunchKernelGGL((scaled_tile_kernel<S, QF, PVEC, WIDE>), dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS),
-                     S::LDS, s, a);
+  hipLaunchKernelGGL(kernel, dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
 }
 

@@ -12,6 +12,8 @@
 //    rows a transposing read takes at once lie in different banks.
 #pragma once
 
+#include <atomic>
+
 #include "linear_common.hpp"
 #include "mr_common.hpp"
 
@@ -264,6 +266,20 @@ struct Walk {
 inline unsigned persistent_blocks(int64_t tiles, int per_cu) {
   const int64_t most = 256 * per_cu;
   return (unsigned)(tiles < most ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : most);
+}
+
+// Once per kernel and device: dynamic LDS beyond 64 KiB.  `done` holds a bit per
+// device.
+template <class K>
+inline hipError_t raise_lds(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Wave roles of a streamed kernel: the last kLoaders waves of a workgroup copy
