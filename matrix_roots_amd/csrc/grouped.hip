@@ -11,10 +11,19 @@
 // memory ("across") go through ds_read_b64_tr_b16, which hands each lane four
 // steps of one column; no transposed copy of a weight is ever made.
 //
-// Row tiles never span two experts.  A launch holds an upper bound of the
-// tiles (rows / tile + experts); every workgroup finds its own from the
-// offsets (one wave scan per 64 experts), so no size reaches the host and the
-// call can be captured and replayed under other sizes.
+// Row tiles never span two experts.  A launch has the
+// workgroups that the CUs hold at a time; each finds its tiles from the offsets
+// (one wave scan over the experts), so no size reaches the host and the call
+// can be captured and replayed under other sizes.
+//
+// What bounds it: the experts' weights (their gradients in float32) come from
+// and go to HBM, and with a few hundred rows per expert that outweighs the
+// products.  So a workgroup's tiles are one stream of chunks: four loader waves
+// copy two chunks ahead, straight to LDS and on into the next tile, and the
+// other four waves never wait for memory.  64 uneven experts, 16384 rows, n =
+// 2048, k = 1536, bf16, one MI355X: forward 147 us (520 MB: 3.5 TB/s), rows'
+// gradient 148 us, weights' gradient 270 us (1.07 GB: 4.0 TB/s); 16 rows 16 us.
+// One workgroup per tile with its own copies took 214, 254 and 440 us.
 #include <type_traits>
 
 #include "tile_core.hpp"
@@ -324,6 +333,7 @@ __device__ __forceinline__ void stream_tiles(Walk w, unsigned char* lds, Load&& 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= S::NW) {
+    __builtin_amdgcn_s_setprio(3);  // copies first: their issue is what the other waves end up waiting for (3%)
     copy_stream<S, PA, QA, FAST>(w, lds, load, wave - S::NW, lane);
     return;
   }
@@ -422,9 +432,12 @@ __device__ __forceinline__ void put_weight(const GroupedArgs& a, O* w, int p0, i
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / S::WQ, wq = wave % S::WQ;
-  if (pv == S::BP && qv == S::BQ && !a.accumulate) {
-    // a whole tile: scalar row addresses, one 32-bit lane offset (with the checks of the general
-    // form below the stores took longer than the products)
+  const int p_left = pv - wp * (S::BP / S::WP), q_left = qv - wq * (S::BQ / S::WQ);
+  if (p_left <= 0 || q_left <= 0) return;
+  if (p_left >= S::BP / S::WP && q_left >= S::BQ / S::WQ && !a.accumulate) {
+    // the wave's part is whole: scalar row addresses, one 32-bit lane offset (with the checks of the
+    // general form below the stores took longer than the products); past the caches, which the
+    // operands need (through them: 300 us for 270)
     O* base = w + (int64_t)(p0 + wp * (S::BP / S::WP)) * a.ldy + q0 + wq * (S::BQ / S::WQ);
     const uint32_t off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)a.ldy + (uint32_t)(lane & 31);
 #pragma unroll
@@ -528,7 +541,6 @@ namespace {
 using Large = GroupedShape<256, 128, 2, 2, 64, 3, 1>;
 using Middle = GroupedShape<128, 64, 2, 2, 64, 4, 1>;
 using Small = GroupedShape<64, 32, 2, 1, 64, 4, 2>;
-using MiddleWeights = GroupedShape<128, 64, 2, 2, 64, 4, 1>;
 using Edge = GroupedShape<128, 128, 2, 2, 64, 4, 1>;
 
 template <class S, typename T, bool TRANSPOSE, bool FAST>
@@ -553,33 +565,42 @@ hipError_t go_weights(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rounds of tiles that the CUs go through, times what a chunk of such a tile
-// takes (in tenths of a microsecond, measured).
+// Rounds of tiles that the CUs go through.
 template <class S>
-int64_t cost(int64_t tiles, int chunk) {
+int64_t rounds(int64_t tiles) {
   const int64_t slots = 256 * S::BPC;
-  return (tiles + slots - 1) / slots * chunk;
+  return (tiles + slots - 1) / slots;
 }
 
+// The tile whose rounds times the time of one of its chunks is least: 1.0, 0.7
+// and 0.65 us for the large, middle and small one.  It decides as the
+// measurements do (large / middle / small tiles, us, n = 2048, k = 1536, bf16):
+// 64 experts with 16384 rows 145 / 226 / 367, with 256 rows 79 / 76 / 75; 8
+// experts with 1024 rows 22 / 16 / 24, with 64 rows 20 / 13 / 12.
 template <typename T, bool TRANSPOSE>
 hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
+  if (!a.fast) return go_rows<Edge, T, TRANSPOSE, false>(a, s);
   const int64_t outs = TRANSPOSE ? a.k : a.n;
   // experts of equal size, as many as can have rows
   const int64_t groups = a.experts < a.rows ? a.experts : a.rows, each = (a.rows + groups - 1) / groups;
   auto tiles = [&](int p, int q) { return groups * ((each + q - 1) / q) * ((outs + p - 1) / p); };
-  if (!a.fast) return go_rows<Edge, T, TRANSPOSE, false>(a, s);
-  const int64_t l = cost<Large>(tiles(256, 128), 10), m = cost<Middle>(tiles(128, 64), 7), n = cost<Small>(tiles(64, 32), 8);
+  const int64_t l = 20 * rounds<Large>(tiles(256, 128)), m = 14 * rounds<Middle>(tiles(128, 64)),
+                n = 13 * rounds<Small>(tiles(64, 32));
   if (n < l && n < m) return go_rows<Small, T, TRANSPOSE, true>(a, s);
   if (m < l) return go_rows<Middle, T, TRANSPOSE, true>(a, s);
   return go_rows<Large, T, TRANSPOSE, true>(a, s);
 }
 
+// Here a tile takes its chunks and its stores: 1.0 us a chunk and 5.4 us for the
+// large tile, 0.45 and 1.4 for the middle one (64 experts with 16384 rows 191 /
+// 290 us, 8 with 4096 rows 42 / 61; 1 with 16384 rows, 1024 x 1024: 155 / 94).
 template <typename T>
 hipError_t pick_weights(const GroupedArgs& a, hipStream_t s) {
-  auto tiles = [&](int p, int q) { return (int64_t)a.experts * ((a.n + p - 1) / p) * ((a.k + q - 1) / q); };
   if (!a.fast) return go_weights<Edge, T, false>(a, s);
-  const int64_t l = cost<Large>(tiles(256, 128), 10), m = cost<MiddleWeights>(tiles(128, 64), 7);
-  return m < l ? go_weights<MiddleWeights, T, true>(a, s) : go_weights<Large, T, true>(a, s);
+  auto tiles = [&](int p, int q) { return (int64_t)a.experts * ((a.n + p - 1) / p) * ((a.k + q - 1) / q); };
+  const int64_t chunks = (a.rows / a.experts + 63) / 64;
+  const int64_t l = rounds<Large>(tiles(256, 128)) * (chunks * 20 + 108), m = rounds<Middle>(tiles(128, 64)) * (chunks * 9 + 28);
+  return m < l ? go_weights<Middle, T, true>(a, s) : go_weights<Large, T, true>(a, s);
 }
 
 }  // namespace
