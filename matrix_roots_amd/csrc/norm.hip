@@ -12,8 +12,11 @@
 // column's: one accumulator per lane over the workgroup's rows, the
 // workgroups' sums added in a fixed order, so no result depends on timing).
 //
-// Both passes move a row once: it stays in registers between the reduction
-// and the output.  A row belongs to one wave (up to 2048 columns) or to the
+// HBM-bound.  Both passes move a row once: it stays in registers between the
+// reduction and the output.  16384 x 2048 bf16, one MI355X: forward with
+// residual, y and e4m3 62 us (304 MB, 4.9 TB/s, what a large copy reaches),
+// gradient 52 us (268 MB, 5.2 TB/s) and 4.6 us for the columns' join; 1 x 1024:
+// 3.3 us, a launch.  A row belongs to one wave (up to 2048 columns) or to the
 // waves of a workgroup (up to 16384).
 #include "linear_common.hpp"
 #include "mr_common.hpp"

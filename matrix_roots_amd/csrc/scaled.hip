@@ -3,19 +3,30 @@
 //
 //   C_ij = sum_b sa_ib sb_jb sum_{l in b} A_il B_jl.
 //
-// Every inner sum of 128 is one v_mfma_f32_16x16x128_f8f6f4; its result is scaled and added to a float32 accumulator by the vector
-// units.  That instruction adds the products of eight steps on a common
+// Every inner sum of 128 is one v_mfma_f32_16x16x128_f8f6f4; its result is
+// scaled and added to a float32 accumulator by the vector units.  That instruction adds the products of eight steps on a common
 // exponent and keeps 17 bits below the largest (measured: next to 2^16 the
 // smallest product that counts is 2^0 among its eight, 2^-7 among the others),
 // an error of about 1e-5 of the result: far below the last place of a 16-bit C,
 // but over 100 of float32.  For a float32 C the operands are therefore widened
 // to fp16 in registers (exactly: both 8-bit types are subsets) and the sums run
-// on v_mfma_f32_16x16x32_f16, which adds in float32, at half the rate.  B is the instruction's row operand
-// ("P"), A its column operand ("Q"): a lane then holds one row of C, so A's
+// on v_mfma_f32_16x16x32_f16, which adds in float32, at half the rate.
+//
+// B is the instruction's row operand ("P"), A its column operand ("Q"): a lane then holds one row of C, so A's
 // scale is one value per lane and column block, B's (one per 128 rows in the
 // square form) one per wave, and their product costs one multiplication per
 // column block beside one FMA per output.  The instruction's order of the 128
 // steps within a lane does not matter, since both operands use the same one.
+//
+// What bounds it (16384 x 8192 x 2048 to bf16, one MI355X): 289 us, 1.90
+// PFLOP/s, against 246 us for the vendor's unscaled 8-bit product.  The matrix
+// instructions alone take about 130 us (4.3 PFLOP/s with four additions each,
+// registers only); the rest is what they wait for: copies into LDS (64 KB a
+// chunk and CU; 247 us without them), the stores of C (32 us, all CUs at once),
+// and the clock, which falls to 2 GHz.  8192 x 2048 x 16383 to float32: 562 us,
+// 0.98 PFLOP/s, on fp16 instructions (1.5 in the vendor's bf16 product) with the
+// widening and two vector operations per result beside them.  8 x 4096 x 1024:
+// 3.8 us, a launch and one pass over 4 MB.
 #include <type_traits>
 
 #include "tile_core.hpp"
@@ -471,62 +482,86 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
 }
 
 // Few rows of C (m <= 16 CB): no tile in LDS.  A workgroup of NW waves owns 16
-// rows of P (16 columns of C); wave w takes the chunks of 128 steps w, w + NW,
+// RB rows of P (columns of C); wave w takes the chunks of 128 steps w, w + NW,
 // ..., straight from global memory into the fragments (P's bytes are read once
 // over the whole launch), and the waves' sums are added through LDS in wave
 // order.
-template <int CB, int NW, int QF, bool PVEC, bool WIDE>
+template <int CB, int RB, int NW, int QF, bool PVEC, bool WIDE>
 __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a) {
-  __shared__ v4f part[NW][CB][64];
+  __shared__ v4f part[NW][RB][CB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i = lane & 15;
-  const int p0 = blockIdx.x * 16;
-  const int pr = min(p0 + i, a.n - 1);
-  const unsigned char* p = a.p + (int64_t)pr * a.ldp;
+  const int p0 = blockIdx.x * 16 * RB;
   const int chunks = (a.k + kChunkBytes - 1) / kChunkBytes;
-  v4f acc[CB];
+  v4f acc[RB][CB];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) acc[cb] = {0.f, 0.f, 0.f, 0.f};
-  auto frag = [&](const unsigned char* row, int c) -> v8i {
-    const int64_t k0 = (int64_t)c * kChunkBytes + 16 * g;
-    const int left = a.k - (int)k0;
-    if (a.fast && c * kChunkBytes + kChunkBytes <= a.k)
-      return join(*reinterpret_cast<const v4i*>(row + k0), *reinterpret_cast<const v4i*>(row + k0 + 64));
-    const v4u u = edge_unit<1>(row + k0, left), v = edge_unit<1>(row + k0 + 64, left - 64);
-    return join(__builtin_bit_cast(v4i, u), __builtin_bit_cast(v4i, v));
-  };
-  for (int c = wave; c < chunks; c += NW) {
-    const typename Frag8<WIDE, 0>::type fp = Frag8<WIDE, 0>::of(frag(p, c));
-    float s[4];
-    if (PVEC) {
+  for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s[v] = a.sp[(int64_t)min(p0 + 4 * g + v, a.n - 1) * a.ldsp + c];
-    } else {
-      s[0] = a.sp[(int64_t)(p0 / kBlock) * a.ldsp + c];
+    for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = {0.f, 0.f, 0.f, 0.f};
+  auto chunk = [&](auto whole_units, int c) {
+    auto frag = [&](const unsigned char* row) -> v8i {
+      const int64_t k0 = (int64_t)c * kChunkBytes + 16 * g;
+      if constexpr (decltype(whole_units)::value)
+        return join(*reinterpret_cast<const v4i*>(row + k0), *reinterpret_cast<const v4i*>(row + k0 + 64));
+      const int left = a.k - (int)k0;
+      const v4u u = edge_unit<1>(row + k0, left), v = edge_unit<1>(row + k0 + 64, left - 64);
+      return join(__builtin_bit_cast(v4i, u), __builtin_bit_cast(v4i, v));
+    };
+    typename Frag8<WIDE, 0>::type fp[RB];
+    float s[RB][PVEC ? 4 : 1];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      fp[rb] = Frag8<WIDE, 0>::of(frag(a.p + (int64_t)min(p0 + rb * 16 + i, a.n - 1) * a.ldp));
+      if (PVEC) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[rb][v] = a.sp[(int64_t)min(p0 + rb * 16 + 4 * g + v, a.n - 1) * a.ldsp + c];
+      } else {
+        s[rb][0] = a.sp[(int64_t)(min(p0 + rb * 16, a.n - 1) / kBlock) * a.ldsp + c];
+      }
     }
+    typename Frag8<WIDE, QF>::type fq[CB];
+    float sc[CB];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
       const int64_t r = min((int64_t)(cb * 16 + i), a.m - 1);
-      const float sc = a.sq[(r >> a.q_shift) * a.ldsq + c];
-      v4f d1[1];
-      const typename Frag8<WIDE, QF>::type fq[1] = {Frag8<WIDE, QF>::of(frag(a.q + r * a.ldq, c))};
-      products<QF>(fp, fq, d1);
-      const v4f d = d1[0];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[cb][v] = fmaf(d[v], sc * s[PVEC ? v : 0], acc[cb][v]);
+      fq[cb] = Frag8<WIDE, QF>::of(frag(a.q + r * a.ldq));
+      sc[cb] = a.sq[(r >> a.q_shift) * a.ldsq + c];
     }
-  }
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) part[wave][cb][lane] = acc[cb];
+    for (int rb = 0; rb < RB; ++rb) {
+      v4f d[CB];
+      products<QF>(fp[rb], fq, d);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[rb][cb][v] = fmaf(d[cb][v], sc[cb] * s[rb][PVEC ? v : 0], acc[rb][cb][v]);
+    }
+  };
+  // whole chunks without a branch, so that the loads of several are in flight
+  const int end = (int)((int64_t)chunks * (blockIdx.y + 1) / a.splits);
+  const int whole = a.fast ? min(a.k / kChunkBytes, end) : 0;
+  int c = (int)((int64_t)chunks * blockIdx.y / a.splits) + wave;
+#pragma unroll 2
+  for (; c < whole; c += NW) chunk(std::true_type{}, c);
+  for (; c < end; c += NW) chunk(std::false_type{}, c);
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) part[wave][rb][cb][lane] = acc[rb][cb];
   __syncthreads();
-  for (int cb = wave; cb < CB; cb += NW) {
-    v4f t = part[0][cb][lane];
+  for (int b = wave; b < RB * CB; b += NW) {
+    const int rb = b / CB, cb = b % CB;
+    v4f t = part[0][rb][cb][lane];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) t += part[w][cb][lane];
+    for (int w = 1; w < NW; ++w) t += part[w][rb][cb][lane];
     const int64_t r = cb * 16 + i;
-    if (r < a.m && p0 + 4 * g < a.n) {
+    const int p = p0 + rb * 16 + 4 * g;
+    if (r < a.m && p < a.n) {
       const float v[4] = {t[0], t[1], t[2], t[3]};
-      put4_as(a.c, r * a.ldc + p0 + 4 * g, v, a.n - p0 - 4 * g, a.c_type, a.vec_c, a.accumulate);
+      if (a.partial)
+        put4(a.partial + ((int64_t)blockIdx.y * a.m + r) * a.n + p, v, a.n - p, a.n % 4 == 0, false);
+      else
+        put4_as(a.c, r * a.ldc + p, v, a.n - p, a.c_type, a.vec_c, a.accumulate);
     }
   }
 }
@@ -576,14 +611,10 @@ hipError_t go_edge(const ScaledArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int CB, int QF, bool PVEC, bool WIDE>
+template <int CB, int RB, int NW, int QF, bool PVEC, bool WIDE>
 hipError_t go_rows(const ScaledArgs& a, hipStream_t s) {
-  const dim3 grid((a.n + 15) / 16);
-  // long contractions under few columns: twice the waves, for bytes in flight
-  if (CB == 1 && grid.x < kCus && a.k >= 32 * kChunkBytes)
-    hipLaunchKernelGGL((scaled_rows_kernel<CB, CB == 1 ? 16 : 8, QF, PVEC, WIDE>), grid, dim3(CB == 1 ? 1024 : 512), 0, s, a);
-  else
-    hipLaunchKernelGGL((scaled_rows_kernel<CB, 8, QF, PVEC, WIDE>), grid, dim3(512), 0, s, a);
+  const dim3 grid((a.n + 16 * RB - 1) / (16 * RB), a.splits);
+  hipLaunchKernelGGL((scaled_rows_kernel<CB, RB, NW, QF, PVEC, WIDE>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 
@@ -592,9 +623,16 @@ hipError_t go_kind(const ScaledArgs& a, int kind, hipStream_t s) {
   if (kind >= 1 && !a.fast) return go_edge<QF, PVEC, WIDE>(a, s);
   if (kind == 2) return go_tile<std::conditional_t<WIDE || PVEC, TileWide, TileLarge>, QF, PVEC, WIDE>(a, s);
   if (kind >= 1) return go_tile<Tile128, QF, PVEC, WIDE>(a, s);
-  if (a.m <= 16) return go_rows<1, QF, PVEC, WIDE>(a, s);
-  if (a.m <= 32) return go_rows<2, QF, PVEC, WIDE>(a, s);
-  return go_rows<4, QF, PVEC, WIDE>(a, s);
+  if (a.m <= 16) {
+    // long contractions under few columns: twice the waves, for bytes in flight
+    if (a.n <= 16 * kCus && a.k / a.splits >= 16 * kChunkBytes) return go_rows<1, 1, 16, QF, PVEC, WIDE>(a, s);
+    return go_rows<1, 1, 8, QF, PVEC, WIDE>(a, s);
+  }
+  // 32 columns to a workgroup halve what is read of A, where enough workgroups are left (64 x 8192 x
+  // 2048: 11.5 us for 15.8; 32 x 4096 x 4096: 12.7 for 10.6)
+  const bool wide = a.n >= 32 * kCus;
+  if (a.m <= 32) return wide ? go_rows<2, 2, 8, QF, PVEC, WIDE>(a, s) : go_rows<2, 1, 8, QF, PVEC, WIDE>(a, s);
+  return wide ? go_rows<4, 2, 8, QF, PVEC, WIDE>(a, s) : go_rows<4, 1, 8, QF, PVEC, WIDE>(a, s);
 }
 
 template <int QF, bool PVEC>
@@ -604,14 +642,24 @@ hipError_t go_width(const ScaledArgs& a, int kind, hipStream_t s) {
 
 }  // namespace
 
+// Up to 64 rows the weights' bytes are all there is to it: no tile (64 x 8192 x
+// 2048: 11.4 us, 17.3 in tiles), the contraction split where the columns leave CUs
+// without work (16 x 1024 x 16384: 11.2 us, 20.3 whole).  256 x 256 tiles once they fill the CUs; below that 128 x 128
+// ones (1024 x 8192 x 8192: 87 us, 110 with large tiles), and a long contraction
+// split while the tiles leave half of the CUs without work (128 x 1024 x 16384: 25
+// us, 94 whole; 2048^3, whose 256 tiles do not: 19 whole, 33 in two parts).
 ScaledPlan scaled_plan(int64_t m, int64_t n, int64_t k) {
-  if (m <= kFewRows) return {0, 1};
   const int64_t chunks = (k + kChunkBytes - 1) / kChunkBytes;
+  if (m <= kFewRows) {
+    int splits = 1;
+    while (splits < 16 && (n + 15) / 16 * splits * 2 <= kCus && chunks / (splits * 2) >= 32) splits *= 2;
+    return {0, splits};
+  }
   auto tiles = [&](int p, int q) { return ((m + q - 1) / q) * ((n + p - 1) / p); };
   if (tiles(256, 256) >= kCus) return {2, 1};
   const int64_t t = tiles(128, 128);
   int64_t splits = 1;
-  while (splits < 16 && t * splits * 2 <= 2 * kCus && chunks / (splits * 2) >= 8) splits *= 2;
+  while (splits < 16 && t * splits * 2 <= kCus && chunks / (splits * 2) >= 8) splits *= 2;
   return {1, (int)splits};
 }
 

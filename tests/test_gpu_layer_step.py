@@ -132,6 +132,24 @@ def test_product_with_nothing_after_the_last_row(dev, m):
     assert torch.equal(mr.block_scaled_matmul(a.q, a.scales, b.q, b.scales), want)
 
 
+@pytest.mark.parametrize("m, n, k", [(3, 100, 9000), (16, 64, 16384), (40, 33, 8200), (200, 120, 12345)])
+def test_product_split_over_a_long_contraction(dev, m, n, k):
+    a = mr.quantize_blocks(randn(dev, 41, m, k))
+    b = mr.quantize_blocks(randn(dev, 42, n, k), block="square")
+    x = a.q.double() * a.scales.double().repeat_interleave(128, 1)[:, :k]
+    w = b.q.double() * b.scales.double().repeat_interleave(128, 1)[:, :k].repeat_interleave(128, 0)[:n]
+    want, mag = x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
+    start = randn(dev, 43, m, n)
+    c = start.clone()
+    mr.block_scaled_matmul(a.q, a.scales, b.q, b.scales, out=c, accumulate=True)
+    # 128 products of a block at 2 U, the blocks, 16 parts, the sum that was there
+    tol = mag * (2 * 128 + (k + 127) // 128 + 3 + 16 + 2) * U + (want + start.double()).abs() * U * 1.01
+    assert bool(((c.double() - (want + start.double())).abs() <= tol + 2.0 ** -24 * start.double().abs()).all())
+    half = mr.block_scaled_matmul(a.q, a.scales, b.q, b.scales)
+    assert bool(((half.double() - want).abs() <= mag * 2.0 ** -14 + want.abs() * 2.0 ** -8 * 1.01).all())
+    assert torch.equal(half, mr.block_scaled_matmul(a.q, a.scales, b.q, b.scales))
+
+
 def test_operators_are_traced(dev):
     B.trace_enable(True)
     try:
