@@ -22,7 +22,7 @@
 // copy two chunks ahead, straight to LDS and on into the next tile, and the
 // other four waves never wait for memory.  64 uneven experts, 16384 rows, n =
 // 2048, k = 1536, bf16, one MI355X: forward 147 us (520 MB: 3.5 TB/s), rows'
-// gradient 148 us, weights' gradient 270 us (1.07 GB: 4.0 TB/s); 16 rows 16 us.
+// gradient 148 us, weights' gradient 210 us (0.92 GB: 4.4 TB/s); 16 rows 16 us.
 // One workgroup per tile with its own copies took 214, 254 and 440 us.
 #include <type_traits>
 
@@ -437,7 +437,7 @@ __device__ __forceinline__ void put_weight(const GroupedArgs& a, O* w, int p0, i
   if (p_left >= S::BP / S::WP && q_left >= S::BQ / S::WQ && !a.accumulate) {
     // the wave's part is whole: scalar row addresses, one 32-bit lane offset (with the checks of the
     // general form below the stores took longer than the products); past the caches, which the
-    // operands need (through them: 300 us for 270)
+    // operands need (through them: 300 us for 270, before operands were read ahead)
     O* base = w + (int64_t)(p0 + wp * (S::BP / S::WP)) * a.ldy + q0 + wq * (S::BQ / S::WQ);
     const uint32_t off = (uint32_t)(4 * (lane >> 5)) * (uint32_t)a.ldy + (uint32_t)(lane & 31);
 #pragma unroll
@@ -509,6 +509,26 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_tile_ke
   }
 }
 
+// Where an expert's rows last a tile for a few chunks only, all CUs of an XCD wait
+// for the same new rows at every expert, each time for a few lines: the operands
+// are brought into the last-level cache at its full rate first.
+// Reads rows first .. last - 1 of `units` 16-byte units once, the grid's waves a row
+// at a time, for the caches' sake.
+__device__ __forceinline__ void read_ahead(const void* base, int64_t ld_bytes, int64_t first, int64_t last, int units, int waves) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint4 all{0, 0, 0, 0};
+  for (int64_t r = first + (int64_t)blockIdx.x * waves + wave; r < last; r += (int64_t)gridDim.x * waves) {
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + r * ld_bytes);
+#pragma unroll 4
+    for (int u = lane; u < units; u += 64) {
+      const uint4 x = row[u];
+      all.x ^= x.x, all.y ^= x.y, all.z ^= x.z, all.w ^= x.w;
+    }
+  }
+  asm volatile("" ::"v"(all.x), "v"(all.y), "v"(all.z), "v"(all.w));  // keeps the loads
+}
+
 template <class S, typename T, bool FAST>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_kernel(const GroupedArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
@@ -532,6 +552,11 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void grouped_weight_
     else
       put_weight<S>(a, reinterpret_cast<T*>(a.y) + t.e * a.y_stride, t.p0, t.pv, (int)t.q0, t.qv, acc);
   };
+  if (FAST && a.ahead) {
+    const int64_t first = offset_at(a, 0), last = offset_at(a, a.experts);
+    read_ahead(a.x, a.ldx * 2, first, last, a.n / 8, S::THREADS / 64);
+    read_ahead(a.w, a.ldw * 2, first, last, a.k / 8, S::THREADS / 64);
+  }
   stream_tiles<S, T, true, true, FAST>(share_experts<S::BK>(a, tp * tq), lds, load, put);
 }
 
@@ -592,11 +617,19 @@ hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
 }
 
 // Here a tile takes its chunks and its stores: 1.0 us a chunk and 5.4 us for the
-// large tile, 0.45 and 1.4 for the middle one (64 experts with 16384 rows 191 /
+// large tile, 0.45 and 1.4 for the middle one (64 equal experts with 16384 rows 191 /
 // 290 us, 8 with 4096 rows 42 / 61; 1 with 16384 rows, 1024 x 1024: 155 / 94).
+// Operands are read ahead where experts have 64 to 512 rows in the mean and the
+// last-level cache (256 MB) holds the operands twice (us with / without, operands
+// out of the caches: 64 experts with 16384 rows 218 / 284, of equal size 191 / 253,
+// with 4096 rows 160 / 177, 8 with 4096 rows 56 / 59; operands in them: 201 / 187
+// at equal size).  Outside it only costs: 64 with 512 rows 156 / 144, 8 with 16384
+// rows 150 / 135, 64 with 32768 rows (n = 4096, 369 MB) 757 / 708.
 template <typename T>
-hipError_t pick_weights(const GroupedArgs& a, hipStream_t s) {
+hipError_t pick_weights(GroupedArgs a, hipStream_t s) {
   if (!a.fast) return go_weights<Edge, T, false>(a, s);
+  a.ahead = a.rows >= 64 * (int64_t)a.experts && a.rows <= 512 * (int64_t)a.experts &&
+            a.rows * (a.n + (int64_t)a.k) * 2 <= 128 * int64_t(1000000);
   auto tiles = [&](int p, int q) { return (int64_t)a.experts * ((a.n + p - 1) / p) * ((a.k + q - 1) / q); };
   const int64_t chunks = (a.rows / a.experts + 63) / 64;
   const int64_t l = rounds<Large>(tiles(256, 128)) * (chunks * 20 + 108), m = rounds<Middle>(tiles(128, 64)) * (chunks * 9 + 28);

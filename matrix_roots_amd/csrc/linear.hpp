@@ -97,6 +97,7 @@ struct GroupedArgs {
   int32_t vec_y;
   int32_t y_f32;
   int32_t accumulate;
+  int32_t ahead;  // the weights' gradient reads its operands once before its tiles (its launcher says)
 };
 // dt: MR_F16 or MR_BF16
 hipError_t launch_grouped(const GroupedArgs& a, mr_dtype dt, bool transpose, hipStream_t s);
