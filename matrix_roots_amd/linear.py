@@ -274,6 +274,8 @@ def grouped_matmul(x, w, offsets, transpose: bool = False, out_dtype=None, out=N
     dev = _device(x, w, offsets, out)
     ldw, w_stride = _bank("w", w)
     experts, n, k = w.shape
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
     rows = x.shape[0]
     if x.dtype != w.dtype:
         raise ValueError("x and w must have one type")
@@ -299,6 +301,8 @@ def grouped_weight_grad(dy, x, offsets, out_dtype=torch.float32, out=None, accum
     dev = _device(dy, x, offsets, out)
     if dy.dtype != x.dtype:
         raise ValueError("dy and x must have one type")
+    if dy.dim() != 2 or x.dim() != 2 or offsets.dim() != 1:
+        raise ValueError("dy and x must be matrices, offsets a vector")
     rows, n = dy.shape
     _same_shape("x", x, (rows, x.shape[1]))
     k = x.shape[1]

@@ -274,3 +274,14 @@ def test_buffers_are_marked_in_use_on_the_callers_stream(fake):
     assert all(u[0] is s for u in fake.used)
     assert fake.calls == ["rms_norm_forward", "rms_norm_backward", "quantize_blocks", "block_scaled_matmul",
                           "grouped_matmul", "grouped_weight_grad"]
+
+
+def test_operands_of_other_dimensions_are_refused(fake):
+    x, w, off = torch.zeros(4, 8).bfloat16(), torch.zeros(2, 8, 8).bfloat16(), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: L.grouped_weight_grad(x[0], x, off), lambda: L.grouped_weight_grad(x, x[0], off),
+                 lambda: L.grouped_weight_grad(x, x, off[0]), lambda: L.grouped_matmul(x, w, off[0]),
+                 lambda: L.grouped_matmul(x[0, 0], w, off), lambda: L.grouped_matmul(x, w[0], off),
+                 lambda: L.quantize_blocks(x[0]), lambda: L.rms_norm_forward(x[0], x[0], 1e-6),
+                 lambda: L.rms_norm_backward(x[0], x[0], x[0].float(), x[0])):
+        with pytest.raises(ValueError):
+            call()
