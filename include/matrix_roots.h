@@ -519,8 +519,8 @@ int32_t mr_set_jacobi_max_sweeps(int32_t sweeps);
  * dimensions are in elements, at most 2^22; row counts may be 0 (then only
  * what the formula makes of an empty sum is written).  Rows at any alignment
  * of their type are accepted; rows whose pointers and leading dimensions are
- * multiples of 16 bytes move in 16-byte units.  Sums are float32; every
- * output is rounded once, to nearest even.  NaN and infinities propagate to
+ * multiples of 16 bytes move in 16-byte units.  Sums are float32, and a float32
+ * result is rounded once to the output's type, to nearest even.  NaN and infinities propagate to
  * the outputs that depend on them and to no others.
  */
 
@@ -534,8 +534,8 @@ int32_t mr_set_jacobi_max_sweeps(int32_t sweeps);
  *   h = x + residual, rounded to dtype (h = x without a residual),
  *   rstd_i = (mean_j h_ij^2 + eps)^(-1/2),  y_ij = h_ij rstd_i weight_j,
  *   scales_ib = max(max_{j in block b} |y_ij|, 2^-100) / F,
- *   q_ij = y_ij / scales_ib rounded to q_dtype, F = 448 (MR_E4M3) or 57344
- *   (MR_E5M2); y in float32 before either rounding.
+ *   q_ij = the float32 quotient y_ij / scales_ib rounded to q_dtype, F = 448
+ *   (MR_E4M3) or 57344 (MR_E5M2); y in float32 before either rounding.
  * width in [1, 16384].  dtype (x, residual, h, y): MR_F32, MR_F16 or MR_BF16;
  * w_dtype: dtype or MR_F32.  h is required with a residual and ignored without
  * one; rstd, y and q (with scales, MR_BLOCK_VECTOR) are each written where not
@@ -584,7 +584,7 @@ mr_status rms_norm_backward(const mr_rms_norm_grad_problem* problem, void* ws, s
 
 /*
  * Quantises X (m x n; x_dtype MR_F32, MR_F16 or MR_BF16) to q_dtype (MR_E4M3 or
- * MR_E5M2) with scales as rms_norm_forward's, in one reading of X:
+ * MR_E5M2) with scales and quotients as rms_norm_forward's, in one reading of X:
  *   Q (m x n) with scales S, blocks along n, and/or
  *   QT (n x m, the transposed order) with scales ST, blocks along m,
  * each where its pointer is not NULL (at least one).  block MR_BLOCK_VECTOR: 1

@@ -126,4 +126,21 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2) {
   return a / (e5m2 ? kE5m2Max : kE4m3Max);
 }
 
+// Values of a block over its scale, the float32 quotient (nearest, ties to even):
+// the product with the rounded reciprocal is at most a place off, and the
+// remainder v - q s, which one fused operation gives exactly, says by how much
+// (Markstein's method).  The product alone turns ties of the 8-bit rounding,
+// which 16-bit inputs meet often.  8191 x 1024 bf16 in both orders: 13.2 us, with
+// the product alone 12.9, with the full division 16.4.  (Values below 2^-102 lose
+// places of the remainder, which ties can stand down to 2^-124.)
+struct Quotient {
+  float inv, s;  // an infinite scale: 0 for finite values, NaN for infinite ones, without its remainder
+  __device__ __forceinline__ explicit Quotient(float scale)
+      : inv(1.f / scale), s(__builtin_isinf(scale) ? 0.f : scale) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, s, v), inv, q);
+  }
+};
+
 }  // namespace mr

@@ -3,7 +3,7 @@
 //
 //   h = x + r (rounded to the stored type), rho = (mean_j h_j^2 + eps)^(-1/2),
 //   y_j = h_j rho w_j,  s_b = max(max_{j in b} |y_j|, 2^-100) / F,
-//   q_j = y_j / s_b rounded to 8 bits (F: the 8-bit type's largest value);
+//   q_j = y_j / s_b (in float32) rounded to 8 bits (F: the 8-bit type's largest value);
 //
 //   dx = dres + rho (g - hh mean_j(g_j hh_j)),  g = dy w,  hh = h rho,
 //   dw_j = sum over rows of dy_j hh_j.
@@ -137,12 +137,12 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_forward_kernel(const N
       if (a.q) {
         amax = max16(amax);
         const float sb = block_scale(amax, a.e5m2);
-        const float inv = 1.f / sb;
+        const Quotient over(sb);
         if (c < a.width && (t & 15) == 0) a.s[r * a.lds + c / kBlock] = sb;
         unsigned char* q = a.q + r * a.ldq + c;
         v2u p;
-        p[0] = pack4(v[k][0] * inv, v[k][1] * inv, v[k][2] * inv, v[k][3] * inv, a.e5m2);
-        p[1] = pack4(v[k][4] * inv, v[k][5] * inv, v[k][6] * inv, v[k][7] * inv, a.e5m2);
+        p[0] = pack4(over(v[k][0]), over(v[k][1]), over(v[k][2]), over(v[k][3]), a.e5m2);
+        p[1] = pack4(over(v[k][4]), over(v[k][5]), over(v[k][6]), over(v[k][7]), a.e5m2);
         if (c + 8 <= a.width) {
           *reinterpret_cast<v2u_any*>(q) = p;
         } else if (c < a.width) {
