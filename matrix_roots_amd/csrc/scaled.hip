@@ -256,9 +256,9 @@ struct ScaledFeed {
   }
 };
 
-// Rows of C (or of a part's partial sums) from the accumulators.
-template <class S, typename O>
-__device__ __forceinline__ void scaled_put(O* c, int64_t ldc, const ScaledTile<S>& t, bool vec, bool accumulate, int wp, int wq,
+// Rows of C (or of a part's partial sums) from the accumulators, through the slab as O.
+template <class S, typename O, typename C>
+__device__ __forceinline__ void scaled_put(C* c, int64_t ldc, const ScaledTile<S>& t, bool vec, bool accumulate, int wp, int wq,
                                            int lane, unsigned char* slab, const v4f (&acc)[S::RB][S::CB]) {
   using W = Slab<O, 16>;
   constexpr int RP = S::RB < W::COLS / 16 ? S::RB : W::COLS / 16;
@@ -288,8 +288,9 @@ __device__ __forceinline__ void scaled_put(O* c, int64_t ldc, const ScaledTile<S
 // product, so that the vector units work under the next products.  The barrier
 // of the next chunk comes before a chunk's last step, whose fragments are in
 // registers by then; Q's fragments of the next chunk are read as the last
-// products release them.
-template <class S, int QF, bool PVEC, bool WIDE>
+// products release them.  ADD: a 16-bit C is added to (a kernel of its own: with both
+// in one the 256 x 256 tile's registers do not do).
+template <class S, int QF, bool PVEC, bool WIDE, bool ADD>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_kernel(const ScaledArgs a) {
   extern __shared__ __align__(256) unsigned char lds[];
   const int lane = threadIdx.x & 63;
@@ -406,13 +407,13 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
 #pragma unroll
     for (int cb = 0; cb < S::CB; ++cb) add(S::RB - 1, cb, sc_old[cb], sr);
     if (S::BP == 128 && a.partial)  // only the small tiles split the contraction
-      scaled_put<S>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
+      scaled_put<S, float>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
     else if constexpr (WIDE)
-      scaled_put<S>(reinterpret_cast<float*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+      scaled_put<S, float>(reinterpret_cast<float*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
     else if (a.c_type == MR_F16)
-      scaled_put<S>(reinterpret_cast<_Float16*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+      scaled_put<S, std::conditional_t<ADD, float, _Float16>>(reinterpret_cast<_Float16*>(a.c), a.ldc, t, a.vec_c, ADD, wp, wq, lane, slab, acc);
     else
-      scaled_put<S>(reinterpret_cast<bf16_t*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+      scaled_put<S, std::conditional_t<ADD, float, bf16_t>>(reinterpret_cast<bf16_t*>(a.c), a.ldc, t, a.vec_c, ADD, wp, wq, lane, slab, acc);
   }
   wait_vmcnt<0>();  // the surplus copies of the last chunk: LDS is given back after them
 }
@@ -471,14 +472,21 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
     }
   }
   unsigned char* slab = lds + S::P_BYTES + S::Q_BYTES + wave * Slab<float, 16>::BYTES;
+  auto put = [&](auto* c) {
+    using C = std::remove_pointer_t<decltype(c)>;
+    if (a.accumulate)
+      scaled_put<S, float>(c, a.ldc, t, a.vec_c, true, wp, wq, lane, slab, acc);
+    else
+      scaled_put<S, C>(c, a.ldc, t, a.vec_c, false, wp, wq, lane, slab, acc);
+  };
   if (a.partial)
-    scaled_put<S>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
+    scaled_put<S, float>(a.partial + (int64_t)t.part * a.m * a.n, (int64_t)a.n, t, a.n % 4 == 0, false, wp, wq, lane, slab, acc);
   else if constexpr (WIDE)
-    scaled_put<S>(reinterpret_cast<float*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+    put(reinterpret_cast<float*>(a.c));
   else if (a.c_type == MR_F16)
-    scaled_put<S>(reinterpret_cast<_Float16*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+    put(reinterpret_cast<_Float16*>(a.c));
   else
-    scaled_put<S>(reinterpret_cast<bf16_t*>(a.c), a.ldc, t, a.vec_c, a.accumulate, wp, wq, lane, slab, acc);
+    put(reinterpret_cast<bf16_t*>(a.c));
 }
 
 // Few rows of C (m <= 16 CB): no tile in LDS.  A workgroup of NW waves owns 16
@@ -593,14 +601,22 @@ using Tile128 = ScaledShape<128, 128, 2, 2, 2>;
 constexpr int kFewRows = 64;
 constexpr int kCus = 256;
 
-template <class S, int QF, bool PVEC, bool WIDE>
-hipError_t go_tile(const ScaledArgs& a, hipStream_t s) {
+template <class S, int QF, bool PVEC, bool WIDE, bool ADD>
+hipError_t launch_tile(const ScaledArgs& a, hipStream_t s) {
   static std::atomic<uint64_t> raised{0};
-  auto kernel = scaled_tile_kernel<S, QF, PVEC, WIDE>;
+  auto kernel = scaled_tile_kernel<S, QF, PVEC, WIDE, ADD>;
   if (hipError_t e = raise_lds(kernel, S::LDS, raised); e != hipSuccess) return e;
   const int64_t tiles = (int64_t)((a.n + S::BP - 1) / S::BP) * ((a.m + S::BQ - 1) / S::BQ) * a.splits;
   hipLaunchKernelGGL(kernel, dim3(persistent_blocks(tiles, S::BPC)), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
+}
+
+template <class S, int QF, bool PVEC, bool WIDE>
+hipError_t go_tile(const ScaledArgs& a, hipStream_t s) {
+  if constexpr (!WIDE) {
+    if (a.accumulate && !a.partial) return launch_tile<S, QF, PVEC, WIDE, true>(a, s);
+  }
+  return launch_tile<S, QF, PVEC, WIDE, false>(a, s);
 }
 
 template <int QF, bool PVEC, bool WIDE>

@@ -218,24 +218,30 @@ struct Slab {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
   }
-  // rows_left x cols_left of the slab exist in c
-  static __device__ __forceinline__ void store(const unsigned char* slab, O* c, int64_t ldc, int rows_left, int cols_left,
+  // rows_left x cols_left of the slab exist in c.  A 16-bit c that is added to takes a
+  // float32 slab, so that the sum is rounded once.
+  template <typename C>
+  static __device__ __forceinline__ void store(const unsigned char* slab, C* c, int64_t ldc, int rows_left, int cols_left,
                                                bool vec, bool accumulate, int lane) {
 #pragma unroll
     for (int j = 0; j < ROWS / 8; ++j) {
       const int row = 8 * j + (lane >> 3), unit = lane & 7, col = unit * EU;
       if (row >= rows_left || col >= cols_left) continue;
       const v4u x = *reinterpret_cast<const v4u*>(slab + row * 128 + (unit ^ (row & 7)) * 16);
-      O* p = c + row * ldc + col;
+      C* p = c + row * ldc + col;
+      O t[EU];
+      __builtin_memcpy(t, &x, 16);
+      if constexpr (sizeof(O) != sizeof(C)) {
+        mr::put4(p, t, cols_left - col, vec, accumulate);
+        continue;
+      }
       if (vec && !accumulate && col + EU <= cols_left) {
         *reinterpret_cast<v4u*>(p) = x;
         continue;
       }
-      O t[EU];
-      __builtin_memcpy(t, &x, 16);
 #pragma unroll
       for (int i = 0; i < EU; ++i)
-        if (col + i < cols_left) p[i] = accumulate ? narrow<O>(widen(t[i]) + widen(p[i])) : t[i];
+        if (col + i < cols_left) p[i] = narrow<C>(accumulate ? widen(t[i]) + widen(p[i]) : widen(t[i]));
     }
   }
 };
