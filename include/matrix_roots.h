@@ -615,7 +615,9 @@ mr_status quantize_blocks(const mr_quantize_problem* problem, void* hip_stream);
  * matrix cores, which add eight products at a time with 17 bits below the
  * largest of them (an error of about 1e-5 of the result); a float32 C on fp16
  * ones, which hold both 8-bit types exactly and add in float32, at half the
- * rate.  Fast where A, B, lda and ldb are multiples of 16 and k is too or
+ * rate.  A block's sum takes SA and then SB (in any order that keeps a result
+ * within float32 where B's are squares), so SA between 2^-100 and 2^95 in
+ * magnitude, or 0, takes no result out of range that is within it.  Fast where A, B, lda and ldb are multiples of 16 and k is too or
  * `padded` is set.  Workspace:
  * block_scaled_matmul_workspace bytes (0 for most sizes), 256-byte aligned.
  */

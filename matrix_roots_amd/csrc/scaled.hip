@@ -12,11 +12,13 @@
 // to fp16 in registers (exactly: both 8-bit types are subsets) and the sums run
 // on v_mfma_f32_16x16x32_f16, which adds in float32, at half the rate.
 //
-// B is the instruction's row operand ("P"), A its column operand ("Q"): a lane then holds one row of C, so A's
-// scale is one value per lane and column block, B's (one per 128 rows in the
-// square form) one per wave, and their product costs one multiplication per
-// column block beside one FMA per output.  The instruction's order of the 128
-// steps within a lane does not matter, since both operands use the same one.
+// B is the instruction's row operand ("P"), A its column operand ("Q"): a lane then
+// holds one row of C, so A's scale is one value per lane and column block, B's (one
+// per 128 rows in the square form) one per wave, and their product costs one
+// multiplication per column block beside one FMA per output.  Where that product is
+// no normal number, and for B's scales by row, a sum takes the two in turn.  The
+// instruction's order of the 128 steps within a lane does not matter, since both
+// operands use the same one.
 //
 // What bounds it (16384 x 8192 x 2048 to bf16, one MI355X): 289 us, 1.90
 // PFLOP/s, against 246 us for the vendor's unscaled 8-bit product.  The matrix
@@ -100,6 +102,41 @@ __device__ __forceinline__ void products(const Wide& p, const Wide (&q)[N], v4f 
       d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p.h[k], q[i].h[k], k == 0 ? zero : d[i], 0, 0, 0);
     }
 }
+
+// Whether a lane's part of a fragment holds anything but zeros.
+__device__ __forceinline__ bool holds_values(v8i x) {
+  int u = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u |= x[i];
+  return (u & 0x7f7f7f7f) != 0;
+}
+__device__ __forceinline__ bool holds_values(const Wide& x) {
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v4i u = __builtin_bit_cast(v4i, x.h[i]);
+    r |= ((u[0] | u[1] | u[2] | u[3]) & 0x7fff7fff) != 0;
+  }
+  return r;
+}
+
+// Scales q and s of a block's sum d, as two factors.  The product of the scales may
+// be past float32's range, or among its subnormal numbers, where d q s is not: then
+// they are taken in turn, first the one that keeps such a result within range.
+struct BothScales {
+  float first = 1.f, then;
+  bool in_turn;
+  __device__ __forceinline__ BothScales(float q, float s) : then(q * s) {
+    constexpr int not_normal = 0x2f7, some = 0x198;  // zero, subnormal, infinite or NaN; finite and not zero
+    in_turn = __builtin_amdgcn_classf(then, not_normal) && __builtin_amdgcn_classf(q, some) && __builtin_amdgcn_classf(s, some);
+    if (in_turn) {
+      const bool q_first = (fabsf(then) > 1.f) == (fabsf(q) < fabsf(s));
+      first = q_first ? q : s;
+      then = q_first ? s : q;
+    }
+  }
+  __device__ __forceinline__ float add(float d, float acc) const { return fmaf(d * first, then, acc); }
+};
 
 __device__ __forceinline__ v8i join(v4i a, v4i b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -317,7 +354,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
     if (!PVEC) {
       const float s = sp[prow];  // the wave's rows of P lie in one square
 #pragma unroll
-      for (int cb = 0; cb < S::CB; ++cb) sc[cb] *= s;
+      for (int cb = 0; cb < S::CB; ++cb) {
+        sc[cb] *= s;
+      }
     }
   };
   auto read_sr = [&](const unsigned char* st, int rb) {
@@ -361,6 +400,44 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
       // their results in registers
       asm volatile("" : "+v"(acc[rb][cb]));
     };
+    // A chunk some of whose scales' products are no normal numbers: sums whose scales are taken in turn
+    // are added here, and nothing for them by the common way.  Q's fragments are in registers, P's come from
+    // LDS again.  Between the first step and the second, after the sums of all chunks before.
+    auto take_in_turn = [&](const unsigned char* st) {
+      int l;  // the lane, worked out here: the loops leave no register for what this needs
+      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+      const float* sq = reinterpret_cast<const float*>(st + S::SQ) + qrow + (l & 15);
+      const float s = reinterpret_cast<const float*>(st + S::SP)[prow];
+      bool any = false;
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) {
+        const bool in_turn = BothScales(sq[cb * 16], s).in_turn;
+        any |= in_turn && holds_values(fq[cb]);  // (zero rows have the smallest scales)
+        if (in_turn) sc[cb] = 0.f;
+      }
+      if (__ballot(any) == 0) return;
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) add(0, cb, sc[cb], sr);
+#pragma unroll
+      for (int rb = 0; rb < S::RB; ++rb) {
+        const typename FP::type fp = FP::of(frag8(st, prow + rb * 16, lane));
+#pragma unroll
+        for (int cb = 0; cb < S::CB; ++cb) {
+          const typename FQ::type one[1] = {fq[cb]};
+          v4f x[1];
+          products<QF>(fp, one, x);
+          const BothScales w(sq[cb * 16], s);
+          if (w.in_turn) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[rb][cb][v] = w.add(x[0][v], acc[rb][cb][v]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb) d[cb] = {0.f, 0.f, 0.f, 0.f};
+      raw = frag8(st, prow + 16, lane);
+    };
     for (int c = t.c_begin; c < t.c_end; ++c) {
       unsigned char* st = lds + (g & 1) * S::STAGE;
       const unsigned char* other = lds + ((g + 1) & 1) * S::STAGE;
@@ -400,6 +477,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
 #pragma unroll
           for (int cb = 0; cb < S::CB; ++cb) sc_old[cb] = sc[cb];
           read_scales(other);
+        }
+        if (!PVEC && rb == 0) {
+          // one comparison for all (magnitudes below the first normal number wrap).  16384 x 8192 x 2048, 1024 x
+          // 8192 x 8192 to bf16: 289, 85 us; 286, 81 without it; 311, 92 with the scales in turn for every sum
+          uint32_t most = 0;
+#pragma unroll
+          for (int cb = 0; cb < S::CB; ++cb) most = umax(most, 2 * __float_as_uint(sc[cb]) - 0x01000000u);
+          if (__builtin_expect(__ballot(most >= 0xfe000000u) != 0, 0)) take_in_turn(st);
         }
       }
       ++g;
@@ -454,7 +539,6 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
       fq[cb] = Frag8<WIDE, QF>::of(frag8(lds + S::P_BYTES, qrow + cb * 16, lane));
       const int64_t r = t.q0 + min(qrow + cb * 16 + (lane & 15), t.qv - 1);
       sc[cb] = a.sq[(r >> a.q_shift) * a.ldsq + c];
-      if (!PVEC) sc[cb] *= a.sp[(int64_t)(t.p0 >> a.p_shift) * a.ldsp + c];
     }
 #pragma unroll
     for (int rb = 0; rb < S::RB; ++rb) {
@@ -464,10 +548,10 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = t.p0 + min(prow + rb * 16 + 4 * (lane >> 4) + v, t.pv - 1);
-        const float s = PVEC ? a.sp[(int64_t)r * a.ldsp + c] : 1.f;
+        const float s = a.sp[(int64_t)(r >> a.p_shift) * a.ldsp + c];
 #pragma unroll
         for (int cb = 0; cb < S::CB; ++cb)
-          acc[rb][cb][v] = PVEC ? fmaf(d[cb][v] * sc[cb], s, acc[rb][cb][v]) : fmaf(d[cb][v], sc[cb], acc[rb][cb][v]);
+          acc[rb][cb][v] = PVEC ? fmaf(d[cb][v] * sc[cb], s, acc[rb][cb][v]) : BothScales(sc[cb], s).add(d[cb][v], acc[rb][cb][v]);
       }
     }
   }
@@ -542,7 +626,9 @@ __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[rb][cb][v] = fmaf(d[cb][v], sc[cb] * s[rb][PVEC ? v : 0], acc[rb][cb][v]);
+        for (int v = 0; v < 4; ++v)
+          acc[rb][cb][v] = PVEC ? fmaf(d[cb][v] * sc[cb], s[rb][v], acc[rb][cb][v])
+                                : BothScales(sc[cb], s[rb][0]).add(d[cb][v], acc[rb][cb][v]);
     }
   };
   // whole chunks without a branch, so that the loads of several are in flight
