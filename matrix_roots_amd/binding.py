@@ -7,6 +7,7 @@ kernels.  A missing library raises; there is no other code path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -324,6 +325,27 @@ def _in_use_on(stream, *tensors):
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+
+
+_as_it_is = contextlib.nullcontext()
+
+
+def _memory_of(stream):
+    """Within it torch takes new tensors from `stream`'s memory.  A block that the
+    current stream's pool hands out may still be read by work queued there, with
+    which `stream` has no order."""
+    import torch
+
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _as_it_is
+
+
+def _in_use_here(stream, *tensors):
+    """Tell torch's caching allocator that results from `stream`'s memory are used
+    by work on the current stream too."""
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream):
+        _in_use_on(torch.cuda.current_stream(), *tensors)
 
 
 def _workspace(nbytes: int, device):

@@ -4,6 +4,9 @@ norm, 8-bit quantisation, block-scaled and expert-grouped products.
 Argument marshalling over libmatrix_roots.so, like binding.py: torch tensors
 provide device memory and the current stream, every step of the computation
 runs in the library's HIP kernels, and nothing waits for the device.
+With `stream` the kernels run there, on inputs that the caller has ordered with
+it; new results come from that stream's memory and are used on the current
+stream once the caller has ordered that.
 Matrices are 2-D with unit column stride.  Nothing here is recorded for
 autograd; the gradients are calls of their own.  Weight gradients come out in
 float32, as gram_ema_update and momentum_ema_batched take them.
@@ -17,7 +20,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import binding as B
-from .binding import _check, _in_use_on, _ptr, _workspace, library
+from .binding import _check, _in_use_here, _in_use_on, _memory_of, _ptr, _workspace, library
 
 _FLOATS = {torch.float32: B.MR_F32, torch.float16: B.MR_F16, torch.bfloat16: B.MR_BF16}
 _EIGHTS = {torch.float8_e4m3fn: B.MR_E4M3, torch.float8_e5m2: B.MR_E5M2}
@@ -126,15 +129,17 @@ def rms_norm_forward(x, weight, eps: float, residual=None, keep_y: bool = True, 
             raise ValueError("residual must have x's type")
     if not keep_y and eight is None:
         raise ValueError("keep_y or eight: one output at least")
-    h = torch.empty(rows, width, dtype=x.dtype, device=dev) if residual is not None else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    y = torch.empty(rows, width, dtype=x.dtype, device=dev) if keep_y else None
-    q = _eight(rows, width, eight, dev) if eight is not None else None
-    scales = torch.empty(rows, _blocks(width), dtype=torch.float32, device=dev) if eight is not None else None
+    with _memory_of(stream):
+        h = torch.empty(rows, width, dtype=x.dtype, device=dev) if residual is not None else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        y = torch.empty(rows, width, dtype=x.dtype, device=dev) if keep_y else None
+        q = _eight(rows, width, eight, dev) if eight is not None else None
+        scales = torch.empty(rows, _blocks(width), dtype=torch.float32, device=dev) if eight is not None else None
     p = B.RmsNormProblem(rows, width, _ptr(x), _ld(x), _ptr(residual), _ld(residual) if residual is not None else 0,
                          _ptr(weight), _ptr(h), width, _ptr(rstd), _ptr(y), width, _ptr(q),
                          (width + 15) // 16 * 16, _ptr(scales), _blocks(width), code, w_code,
                          _EIGHTS[q.dtype] if q is not None else 0, 0, float(eps))
+    _in_use_here(stream, h, rstd, y, q, scales)
     _in_use_on(stream, h, rstd, y, q, scales)
     _check(library().rms_norm_forward(addressof(p), _stream(stream, dev)))
     return RmsNormOut(h if residual is not None else x, rstd, y, q, scales)
@@ -155,14 +160,17 @@ def rms_norm_backward(dy, h, rstd, weight, dresidual=None, weight_grad: bool = T
     if rstd.dtype != torch.float32 or rstd.dim() != 1 or rstd.shape[0] != rows or (rows > 1 and rstd.stride(0) != 1):
         raise ValueError("rstd must be contiguous float32, one value per row")
     w_code = _norm_weight(weight, dy)
-    dx = torch.empty(rows, width, dtype=dy.dtype, device=dev)
-    dweight = torch.empty(width, dtype=torch.float32, device=dev) if weight_grad else None
+    with _memory_of(stream):
+        dx = torch.empty(rows, width, dtype=dy.dtype, device=dev)
+        dweight = torch.empty(width, dtype=torch.float32, device=dev) if weight_grad else None
     p = B.RmsNormGradProblem(rows, width, _ptr(dy), _ld(dy), _ptr(h), _ld(h), _ptr(rstd), _ptr(weight),
                              _ptr(dresidual), _ld(dresidual) if dresidual is not None else 0, _ptr(dx), width,
                              _ptr(dweight), code, w_code)
     lib = library()
     need = lib.rms_norm_backward_workspace(addressof(p))
-    ws = _workspace(need, dev)
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
+    _in_use_here(stream, dx, dweight)
     _in_use_on(stream, ws, dx, dweight)
     _check(lib.rms_norm_backward(addressof(p), _ptr(ws), need, _stream(stream, dev)))
     return dx, dweight
@@ -185,15 +193,17 @@ def quantize_blocks(x, eight: str = "e4m3", block: str = "vector", order: str = 
     m, n = x.shape
     square = block == "square"
     q = s = qt = st = None
-    if order != "columns":
-        q = _eight(m, n, eight, dev)
-        s = torch.empty(_blocks(m) if square else m, _blocks(n), dtype=torch.float32, device=dev)
-    if order != "rows":
-        qt = _eight(n, m, eight, dev)
-        st = torch.empty(_blocks(n) if square else n, _blocks(m), dtype=torch.float32, device=dev)
+    with _memory_of(stream):
+        if order != "columns":
+            q = _eight(m, n, eight, dev)
+            s = torch.empty(_blocks(m) if square else m, _blocks(n), dtype=torch.float32, device=dev)
+        if order != "rows":
+            qt = _eight(n, m, eight, dev)
+            st = torch.empty(_blocks(n) if square else n, _blocks(m), dtype=torch.float32, device=dev)
     p = B.QuantizeProblem(m, n, _ptr(x), _ld(x), _ptr(q), (n + 15) // 16 * 16, _ptr(s), _blocks(n), _ptr(qt),
                           (m + 15) // 16 * 16, _ptr(st), _blocks(m), code, _EIGHTS[(q if q is not None else qt).dtype],
                           _BLOCKS[block], 0)
+    _in_use_here(stream, q, s, qt, st)
     _in_use_on(stream, q, s, qt, st)
     _check(library().quantize_blocks(addressof(p), _stream(stream, dev)))
     return Quantized(q, s, qt, st)
@@ -233,7 +243,8 @@ def block_scaled_matmul(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, accumu
     if own:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(m, n, dtype=out_dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(m, n, dtype=out_dtype, device=dev)
     else:
         _same_shape("out", out, (m, n))
     lda, ldb = _ld(a), _ld(b)
@@ -243,7 +254,10 @@ def block_scaled_matmul(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, accumu
                               1 if accumulate else 0, 1 if padded else 0, 0)
     lib = library()
     need = lib.block_scaled_matmul_workspace(addressof(p))
-    ws = _workspace(need, dev)
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
+    if own:
+        _in_use_here(stream, out)
     _in_use_on(stream, ws, out if own else None)
     _check(lib.block_scaled_matmul(addressof(p), _ptr(ws), need, _stream(stream, dev)))
     return out
@@ -283,7 +297,9 @@ def grouped_matmul(x, w, offsets, transpose: bool = False, out_dtype=None, out=N
     bits = _offset_bits(offsets, experts)
     own = out is None
     if own:
-        out = torch.empty(rows, k if transpose else n, dtype=out_dtype or x.dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(rows, k if transpose else n, dtype=out_dtype or x.dtype, device=dev)
+        _in_use_here(stream, out)
     else:
         _same_shape("out", out, (rows, k if transpose else n))
     p = B.GroupedProblem(experts, rows, n, k, _ptr(x), _ld(x), _ptr(w), ldw, w_stride, _ptr(offsets), _ptr(out),
@@ -312,7 +328,9 @@ def grouped_weight_grad(dy, x, offsets, out_dtype=torch.float32, out=None, accum
     if own:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(experts, n, k, dtype=out_dtype, device=dev)
+        with _memory_of(stream):
+            out = torch.empty(experts, n, k, dtype=out_dtype, device=dev)
+        _in_use_here(stream, out)
     else:
         _same_shape("out", out, (experts, n, k))
     ld, stride = _bank("out", out)
