@@ -445,13 +445,16 @@ def _root_call(entry, size_entry, code, As, eps, normalize, Xs, workspace, strea
     dev = As[0].device
     own_x = Xs is None
     if own_x:
-        Xs = [torch.empty(d, d, dtype=torch.float32, device=dev) for d, _, _ in syms]
+        with _memory_of(stream):
+            Xs = [torch.empty(d, d, dtype=torch.float32, device=dev) for d, _, _ in syms]
+        _in_use_here(stream, *Xs)
     probs = (RootProblem * count)()
     for i, (A, X) in enumerate(zip(As, Xs)):
         probs[i] = RootProblem(syms[i][0], _ptr(A), syms[i][1], _ptr(X), _ld(X))
     need = size_entry(ctypes.addressof(probs), count, dt, code)
     ws = workspace or RootWorkspace()
-    buf, info = ws.get(need, count, dev)
+    with _memory_of(stream):
+        buf, info = ws.get(need, count, dev)
     if info_out is not None:
         if info_out.numel() < ROOT_INFO_BYTES * count:
             raise ValueError("info_out too small")
@@ -530,14 +533,17 @@ def polar_cans_batched(Gs: Sequence, precision: str = "f16", Os: Optional[Sequen
     dev = Gs[0].device
     own_o = Os is None
     if own_o:
-        Os = [torch.empty_like(G) for G in Gs]
+        with _memory_of(stream):
+            Os = [torch.empty_like(G) for G in Gs]
+        _in_use_here(stream, *Os)
     probs = (PolarProblem * count)()
     for i, (G, O) in enumerate(zip(Gs, Os)):
         probs[i] = PolarProblem(G.shape[0], G.shape[1], _ptr(G), _ld(G), _ptr(O), _ld(O))
     code = _PRECISIONS[precision]
     need = lib.polar_cans_batched_workspace(ctypes.addressof(probs), count, code)
     ws = workspace or RootWorkspace()
-    buf, info = ws.get(need, count, dev)
+    with _memory_of(stream):
+        buf, info = ws.get(need, count, dev)
     if info_out is not None:
         if info_out.numel() < ROOT_INFO_BYTES * count:
             raise ValueError("info_out too small")
@@ -583,8 +589,10 @@ def hyperball_update_batched(Ws: Sequence, Us: Sequence, lr: float, return_norms
             raise ValueError("W and U shapes differ")
         probs[i] = HyperballProblem(W.shape[0], W.shape[1], _ptr(W), _ld(W), _ptr(U), _ld(U))
     need = lib.hyperball_update_batched_workspace(ctypes.addressof(probs), count)
-    ws = _workspace(need, dev)
-    norms = torch.empty(count, 3, dtype=torch.float64, device=dev) if return_norms else None
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
+        norms = torch.empty(count, 3, dtype=torch.float64, device=dev) if return_norms else None
+    _in_use_here(stream, norms)
     _in_use_on(stream, ws, norms)
     _check(lib.hyperball_update_batched(ctypes.addressof(probs), count, float(lr), _ptr(norms), _ptr(ws), need,
                                         _stream(stream)))
@@ -616,14 +624,17 @@ def precondition_apply(XLs: Sequence, Gs: Sequence, XRs: Sequence, alpha: float 
     dev = Gs[0].device
     own_u = Us is None
     if own_u:
-        Us = [torch.empty_like(G) for G in Gs]
+        with _memory_of(stream):
+            Us = [torch.empty_like(G) for G in Gs]
+        _in_use_here(stream, *Us)
     probs = (ApplyProblem * count)()
     for i in range(count):
         XL, G, XR, U = XLs[i], Gs[i], XRs[i], Us[i]
         probs[i] = ApplyProblem(G.shape[0], G.shape[1], _ptr(XL), _ld(XL), _ptr(G), _ld(G), _ptr(XR), _ld(XR),
                                 _ptr(U), _ld(U))
     need = lib.precondition_apply_workspace(ctypes.addressof(probs), count)
-    ws = _workspace(need, dev)
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
     _in_use_on(stream, ws, *(Us if own_u else ()))
     _check(lib.precondition_apply(ctypes.addressof(probs), count, float(alpha), _ptr(ws), need, _stream(stream)))
     return Us
