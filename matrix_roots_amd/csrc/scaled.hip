@@ -4,13 +4,18 @@
 //   C_ij = sum_b sa_ib sb_jb sum_{l in b} A_il B_jl.
 //
 // Every inner sum of 128 is one v_mfma_f32_16x16x128_f8f6f4; its result is
-// scaled and added to a float32 accumulator by the vector units.  That instruction adds the products of eight steps on a common
-// exponent and keeps 17 bits below the largest (measured: next to 2^16 the
-// smallest product that counts is 2^0 among its eight, 2^-7 among the others),
-// an error of about 1e-5 of the result: far below the last place of a 16-bit C,
-// but over 100 of float32.  For a float32 C the operands are therefore widened
-// to fp16 in registers (exactly: both 8-bit types are subsets) and the sums run
-// on v_mfma_f32_16x16x32_f16, which adds in float32, at half the rate.
+// scaled and added to a float32 accumulator by the vector units.  That instruction
+// adds the products of eight steps on a common exponent and cuts them at 2^-13 of
+// the largest one's power of two (next to 2^16 and -2^16 the smallest product that
+// counts is 2^3 among their eight, 2^-7 among the others): in the sum of
+// magnitudes at most 2^-10, measured 1e-5 at most, and 1.4e-5 to 1.8e-5 of the
+// results in the mean square (random and activation-like operands, k = 2048 and
+// 8192).  A 16-bit C's own rounding is 1.7e-3 (bf16), 2.1e-4 (fp16) there; where
+// large products cancel, what is left loses those places.  A float32 C shows them
+// always, and for few rows the bytes bound the product: there the operands are
+// widened to fp16 in registers (exactly: both 8-bit types are subsets) and the
+// sums run on v_mfma_f32_16x16x32_f16, which adds in float32, at half the rate
+// (6e-8 of the results).
 //
 // B is the instruction's row operand ("P"), A its column operand ("Q"): a lane then
 // holds one row of C, so A's scale is one value per lane and column block, B's (one
@@ -577,8 +582,10 @@ __global__ __launch_bounds__(256) void scaled_edge_kernel(const ScaledArgs a) {
 // RB rows of P (columns of C); wave w takes the chunks of 128 steps w, w + NW,
 // ..., straight from global memory into the fragments (P's bytes are read once
 // over the whole launch), and the waves' sums are added through LDS in wave
-// order.
-template <int CB, int RB, int NW, int QF, bool PVEC, bool WIDE>
+// order.  The bytes take the time, so every C is summed on fp16 instructions (in
+// 8 bits the same: 8 x 4096 x 1024 3.5 us, 64 x 8192 x 2048 11.4; 48 x 8192 x 8192
+// 28.3 for 29.6).
+template <int CB, int RB, int NW, int QF, bool PVEC>
 __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a) {
   __shared__ v4f part[NW][RB][CB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -599,11 +606,11 @@ __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a
       const v4u u = edge_unit<1>(row + k0, left), v = edge_unit<1>(row + k0 + 64, left - 64);
       return join(__builtin_bit_cast(v4i, u), __builtin_bit_cast(v4i, v));
     };
-    typename Frag8<WIDE, 0>::type fp[RB];
+    typename Frag8<true, 0>::type fp[RB];
     float s[RB][PVEC ? 4 : 1];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      fp[rb] = Frag8<WIDE, 0>::of(frag(a.p + (int64_t)min(p0 + rb * 16 + i, a.n - 1) * a.ldp));
+      fp[rb] = Frag8<true, 0>::of(frag(a.p + (int64_t)min(p0 + rb * 16 + i, a.n - 1) * a.ldp));
       if (PVEC) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) s[rb][v] = a.sp[(int64_t)min(p0 + rb * 16 + 4 * g + v, a.n - 1) * a.ldsp + c];
@@ -611,12 +618,12 @@ __global__ __launch_bounds__(64 * NW) void scaled_rows_kernel(const ScaledArgs a
         s[rb][0] = a.sp[(int64_t)(min(p0 + rb * 16, a.n - 1) / kBlock) * a.ldsp + c];
       }
     }
-    typename Frag8<WIDE, QF>::type fq[CB];
+    typename Frag8<true, QF>::type fq[CB];
     float sc[CB];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
       const int64_t r = min((int64_t)(cb * 16 + i), a.m - 1);
-      fq[cb] = Frag8<WIDE, QF>::of(frag(a.q + r * a.ldq));
+      fq[cb] = Frag8<true, QF>::of(frag(a.q + r * a.ldq));
       sc[cb] = a.sq[(r >> a.q_shift) * a.ldsq + c];
     }
 #pragma unroll
@@ -713,10 +720,10 @@ hipError_t go_edge(const ScaledArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int CB, int RB, int NW, int QF, bool PVEC, bool WIDE>
+template <int CB, int RB, int NW, int QF, bool PVEC>
 hipError_t go_rows(const ScaledArgs& a, hipStream_t s) {
   const dim3 grid((a.n + 16 * RB - 1) / (16 * RB), a.splits);
-  hipLaunchKernelGGL((scaled_rows_kernel<CB, RB, NW, QF, PVEC, WIDE>), grid, dim3(64 * NW), 0, s, a);
+  hipLaunchKernelGGL((scaled_rows_kernel<CB, RB, NW, QF, PVEC>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 
@@ -727,14 +734,14 @@ hipError_t go_kind(const ScaledArgs& a, int kind, hipStream_t s) {
   if (kind >= 1) return go_tile<Tile128, QF, PVEC, WIDE>(a, s);
   if (a.m <= 16) {
     // long contractions under few columns: twice the waves, for bytes in flight
-    if (a.n <= 16 * kCus && a.k / a.splits >= 16 * kChunkBytes) return go_rows<1, 1, 16, QF, PVEC, WIDE>(a, s);
-    return go_rows<1, 1, 8, QF, PVEC, WIDE>(a, s);
+    if (a.n <= 16 * kCus && a.k / a.splits >= 16 * kChunkBytes) return go_rows<1, 1, 16, QF, PVEC>(a, s);
+    return go_rows<1, 1, 8, QF, PVEC>(a, s);
   }
   // 32 columns to a workgroup halve what is read of A, where enough workgroups are left (64 x 8192 x
   // 2048: 11.5 us for 15.8; 32 x 4096 x 4096: 12.7 for 10.6)
   const bool wide = a.n >= 32 * kCus;
-  if (a.m <= 32) return wide ? go_rows<2, 2, 8, QF, PVEC, WIDE>(a, s) : go_rows<2, 1, 8, QF, PVEC, WIDE>(a, s);
-  return wide ? go_rows<4, 2, 8, QF, PVEC, WIDE>(a, s) : go_rows<4, 1, 8, QF, PVEC, WIDE>(a, s);
+  if (a.m <= 32) return wide ? go_rows<2, 2, 8, QF, PVEC>(a, s) : go_rows<2, 1, 8, QF, PVEC>(a, s);
+  return wide ? go_rows<4, 2, 8, QF, PVEC>(a, s) : go_rows<4, 1, 8, QF, PVEC>(a, s);
 }
 
 template <int QF, bool PVEC>
