@@ -10,9 +10,6 @@ torch = pytest.importorskip("torch")
 import matrix_roots_amd as mr  # noqa: E402
 from matrix_roots_amd import binding as B  # noqa: E402
 
-U = 2.0 ** -24
-H = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
-TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
 E4 = torch.float8_e4m3fn
 # few rows, 128 x 128 tiles, large tiles, split contractions, and sizes that are no whole 16-byte units
 SIZES = [(5, 96, 384), (50, 77, 200), (300, 200, 256), (290, 130, 211), (4200, 4100, 192), (16, 64, 8192), (200, 120, 4096)]
@@ -34,22 +31,22 @@ def randn(dev, seed, *shape):
 @pytest.mark.parametrize("b_square", [False, True])
 @pytest.mark.parametrize("m, n, k", SIZES)
 def test_one_rounding(dev, m, n, k, b_square, t):
-    """C nearly cancels the product, so a rounding of the product alone would be most of what is left."""
-    a = mr.quantize_blocks(randn(dev, 1, m, k).abs())
-    b = mr.quantize_blocks(randn(dev, 2, n, k).abs(), block="square" if b_square else "vector")
-    x = a.q.double() * a.scales.double().repeat_interleave(128, 1)[:, :k]
-    sb = b.scales.double().repeat_interleave(128, 1)[:, :k]
-    y = b.q.double() * (sb.repeat_interleave(128, 0)[:n] if b_square else sb)
-    product = x @ y.t().contiguous()  # its terms are positive: their magnitudes' sum too
-    for pad in (0, 3):  # rows of C in whole 16-byte units or not
+    """C nearly cancels the product, so a rounding of the product alone would be most of what is left.  Operands between
+    1 and 2 with 3 binary places: products have 6 and sums are below 2^14, exact in float32 and on 8-bit cores alike."""
+    a, b = (1 + randn(dev, seed, rows, k).abs().remainder(1).mul(8).floor() / 8 for seed, rows in ((1, m), (2, n)))
+    kb = (k + 127) // 128
+    sa, sb = torch.ones(m, kb, device=dev), torch.ones((n + 127) // 128 if b_square else n, kb, device=dev)
+    product = a.double() @ b.double().t().contiguous()
+    # whole 16-byte units, rows of C that are none, rows of A and B that are none
+    for pad, odd in ((0, 0), (3, 0), (0, 5)):
+        x, y = (torch.zeros(v.shape[0], (k + 15) // 16 * 16 + odd, device=dev).to(E4)[:, :k] for v in (a, b))
+        x.copy_(a)
+        y.copy_(b)
         c = torch.zeros(m, n + pad, dtype=t, device=dev)[:, :n]
         c.copy_(-product)
-        want = product + c.double()
-        mr.block_scaled_matmul(a.q, a.scales, b.q, b.scales, out=c, accumulate=True)
-        # eight products together keep 17 bits below the largest: 8 2^-17 of the sum; then float32 sums, one rounding to t
-        tol = product * (2.0 ** -14 + (2 * 128 + (k + 127) // 128 + 19) * U) + want.abs() * H[t] * 1.01 + TINY[t]
-        off = (c.double() - want).abs() > tol
-        assert not bool(off.any()), f"{int(off.sum())} of {off.numel()} off, worst {float(((c.double() - want).abs() / tol).max()):.3g} x tolerance"
+        want = (product + c.double()).to(t)
+        mr.block_scaled_matmul(x, sa, y, sb, out=c, accumulate=True)
+        assert torch.equal(c, want), f"{int((c != want).sum())} of {c.numel()} off"
 
 
 @pytest.mark.parametrize("m, n", [(8, 64), (300, 200), (4200, 4100)])
