@@ -620,16 +620,28 @@ hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
 // large tile, 0.45 and 1.4 for the middle one (64 equal experts with 16384 rows 191 /
 // 290 us, 8 with 4096 rows 42 / 61; 1 with 16384 rows, 1024 x 1024: 155 / 94).
 // Operands are read ahead where experts have 64 to 512 rows in the mean and the
-// last-level cache (256 MB) holds the operands twice (us with / without, operands
-// out of the caches: 64 experts with 16384 rows 218 / 284, of equal size 191 / 253,
-// with 4096 rows 160 / 177, 8 with 4096 rows 56 / 59; operands in them: 201 / 187
-// at equal size).  Outside it only costs: 64 with 512 rows 156 / 144, 8 with 16384
-// rows 150 / 135, 64 with 32768 rows (n = 4096, 369 MB) 757 / 708.
+// last-level cache (256 MB) holds the operands.  us without / with, 64 uneven
+// experts of 2048 x 1536 unless said, behind the rows' gradient, which has just
+// read dy, and with nothing in the caches:
+//   rows (operands)            behind the rows' gradient   cold
+//   2048 (15 MB)               159 / 161                   154 / 161
+//   4096 (29 MB)               164 / 158                   172 / 161
+//   16384 (117 MB)             263 / 210                   301 / 218
+//   16384, 3328 x 2560 (193)   715 / 498                   782 / 529
+//   32768 (235)                358 / 323                   398 / 348
+//   32768, 2048 x 1792 (252)   404 / 390                   446 / 398
+//   32768, 2560 x 2048 (302)   673 / 717                   723 / 767
+//   8 experts, 4096 (29)       66 / 59                     72 / 62
+//   16, 8192, 2048 x 2048 (67) 126 / 127                   155 / 129
+//   24, 24576 (176)            206 / 232                   254 / 254
+//   32, 32768 (235)            257 / 283                   320 / 312
+// With both operands already in the caches it costs 7% (16384 rows, experts of equal
+// size: 201 / 187).
 template <typename T>
 hipError_t pick_weights(GroupedArgs a, hipStream_t s) {
   if (!a.fast) return go_weights<Edge, T, false>(a, s);
   a.ahead = a.rows >= 64 * (int64_t)a.experts && a.rows <= 512 * (int64_t)a.experts &&
-            a.rows * (a.n + (int64_t)a.k) * 2 <= 128 * int64_t(1000000);
+            a.rows * (a.n + (int64_t)a.k) * 2 <= 256 * int64_t(1000000);
   auto tiles = [&](int p, int q) { return (int64_t)a.experts * ((a.n + p - 1) / p) * ((a.k + q - 1) / q); };
   const int64_t chunks = (a.rows / a.experts + 63) / 64;
   const int64_t l = rounds<Large>(tiles(256, 128)) * (chunks * 20 + 108), m = rounds<Middle>(tiles(128, 64)) * (chunks * 9 + 28);
