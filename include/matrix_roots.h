@@ -590,7 +590,8 @@ mr_status rms_norm_backward(const mr_rms_norm_grad_problem* problem, void* ws, s
  * each where its pointer is not NULL (at least one).  block MR_BLOCK_VECTOR: 1
  * x 128 blocks of Q's and of QT's own rows (S: m x ceil(n/128), ST: n x
  * ceil(m/128)); MR_BLOCK_SQUARE: 128 x 128 squares, the same in both orders (S:
- * ceil(m/128) x ceil(n/128), ST its transpose).  A block that holds a NaN or an
+ * ceil(m/128) x ceil(n/128), ST its transpose).  Less than 2^23 squares of 128 x
+ * 128 in one call.  A block that holds a NaN or an
  * infinity stands for NaN throughout.
  */
 typedef struct {

@@ -194,7 +194,8 @@ mr_status quantize_blocks(const mr_quantize_problem* p, void* hip_stream) {
   const size_t es = size_of(p->x_dtype);
   const int64_t mb = blocks128(p->m), nb = blocks128(p->n);
   const bool square = p->block == MR_BLOCK_SQUARE;
-  if (mb * nb >= (int64_t(1) << 31)) return fail(MR_ERR_SHAPE, "%lld blocks", (long long)(mb * nb));
+  // a workgroup of 512 threads for each; a launch has less than 2^32 threads
+  if (mb * nb >= (int64_t(1) << 23)) return fail(MR_ERR_SHAPE, "%lld blocks of 128 x 128 in one call", (long long)(mb * nb));
   MR_TRY(check_matrix("X", p->X, p->n, p->ldx, es));
   Aliases al;
   al.in("X", p->X, p->m, p->n, p->ldx, es);
