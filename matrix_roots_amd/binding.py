@@ -334,6 +334,8 @@ def _memory_of(stream):
     """Within it torch takes new tensors from `stream`'s memory.  A block that the
     current stream's pool hands out may still be read by work queued there, with
     which `stream` has no order."""
+    if stream is None:
+        return _as_it_is
     import torch
 
     return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _as_it_is
@@ -342,6 +344,8 @@ def _memory_of(stream):
 def _in_use_here(stream, *tensors):
     """Tell torch's caching allocator that results from `stream`'s memory are used
     by work on the current stream too."""
+    if stream is None:
+        return
     import torch
 
     if isinstance(stream, torch.cuda.Stream):

@@ -139,8 +139,9 @@ def rms_norm_forward(x, weight, eps: float, residual=None, keep_y: bool = True, 
                          _ptr(weight), _ptr(h), width, _ptr(rstd), _ptr(y), width, _ptr(q),
                          (width + 15) // 16 * 16, _ptr(scales), _blocks(width), code, w_code,
                          _EIGHTS[q.dtype] if q is not None else 0, 0, float(eps))
-    _in_use_here(stream, h, rstd, y, q, scales)
-    _in_use_on(stream, h, rstd, y, q, scales)
+    if stream is not None:
+        _in_use_here(stream, h, rstd, y, q, scales)
+        _in_use_on(stream, h, rstd, y, q, scales)
     _check(library().rms_norm_forward(addressof(p), _stream(stream, dev)))
     return RmsNormOut(h if residual is not None else x, rstd, y, q, scales)
 
@@ -170,8 +171,9 @@ def rms_norm_backward(dy, h, rstd, weight, dresidual=None, weight_grad: bool = T
     need = lib.rms_norm_backward_workspace(addressof(p))
     with _memory_of(stream):
         ws = _workspace(need, dev)
-    _in_use_here(stream, dx, dweight)
-    _in_use_on(stream, ws, dx, dweight)
+    if stream is not None:
+        _in_use_here(stream, dx, dweight)
+        _in_use_on(stream, ws, dx, dweight)
     _check(lib.rms_norm_backward(addressof(p), _ptr(ws), need, _stream(stream, dev)))
     return dx, dweight
 
@@ -203,8 +205,9 @@ def quantize_blocks(x, eight: str = "e4m3", block: str = "vector", order: str = 
     p = B.QuantizeProblem(m, n, _ptr(x), _ld(x), _ptr(q), (n + 15) // 16 * 16, _ptr(s), _blocks(n), _ptr(qt),
                           (m + 15) // 16 * 16, _ptr(st), _blocks(m), code, _EIGHTS[(q if q is not None else qt).dtype],
                           _BLOCKS[block], 0)
-    _in_use_here(stream, q, s, qt, st)
-    _in_use_on(stream, q, s, qt, st)
+    if stream is not None:
+        _in_use_here(stream, q, s, qt, st)
+        _in_use_on(stream, q, s, qt, st)
     _check(library().quantize_blocks(addressof(p), _stream(stream, dev)))
     return Quantized(q, s, qt, st)
 
@@ -254,11 +257,13 @@ def block_scaled_matmul(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, accumu
                               1 if accumulate else 0, 1 if padded else 0, 0)
     lib = library()
     need = lib.block_scaled_matmul_workspace(addressof(p))
-    with _memory_of(stream):
-        ws = _workspace(need, dev)
-    if own:
-        _in_use_here(stream, out)
-    _in_use_on(stream, ws, out if own else None)
+    ws = None
+    if need:
+        with _memory_of(stream):
+            ws = _workspace(need, dev)
+    if stream is not None:
+        _in_use_here(stream, out if own else None)
+        _in_use_on(stream, ws, out if own else None)
     _check(lib.block_scaled_matmul(addressof(p), _ptr(ws), need, _stream(stream, dev)))
     return out
 
@@ -299,12 +304,13 @@ def grouped_matmul(x, w, offsets, transpose: bool = False, out_dtype=None, out=N
     if own:
         with _memory_of(stream):
             out = torch.empty(rows, k if transpose else n, dtype=out_dtype or x.dtype, device=dev)
-        _in_use_here(stream, out)
     else:
         _same_shape("out", out, (rows, k if transpose else n))
     p = B.GroupedProblem(experts, rows, n, k, _ptr(x), _ld(x), _ptr(w), ldw, w_stride, _ptr(offsets), _ptr(out),
                          _ld(out), _float_code(x, "x"), _float_code(out, "out"), bits, 1 if transpose else 0)
-    _in_use_on(stream, out if own else None)
+    if stream is not None and own:
+        _in_use_here(stream, out)
+        _in_use_on(stream, out)
     _check(library().grouped_matmul(addressof(p), _stream(stream, dev)))
     return out
 
@@ -330,12 +336,13 @@ def grouped_weight_grad(dy, x, offsets, out_dtype=torch.float32, out=None, accum
             raise ValueError("accumulate needs out")
         with _memory_of(stream):
             out = torch.empty(experts, n, k, dtype=out_dtype, device=dev)
-        _in_use_here(stream, out)
     else:
         _same_shape("out", out, (experts, n, k))
     ld, stride = _bank("out", out)
     p = B.GroupedGradProblem(experts, rows, n, k, _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(offsets), _ptr(out), ld,
                              stride, _float_code(dy, "dy"), _float_code(out, "out"), bits, 1 if accumulate else 0)
-    _in_use_on(stream, out if own else None)
+    if stream is not None and own:
+        _in_use_here(stream, out)
+        _in_use_on(stream, out)
     _check(library().grouped_weight_grad(addressof(p), _stream(stream, dev)))
     return out
