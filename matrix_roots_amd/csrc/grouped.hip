@@ -22,7 +22,8 @@
 // copy two chunks ahead, straight to LDS and on into the next tile, and the
 // other four waves never wait for memory.  64 uneven experts, 16384 rows, n =
 // 2048, k = 1536, bf16, one MI355X: forward 147 us (520 MB: 3.5 TB/s), rows'
-// gradient 148 us, weights' gradient 210 us (0.92 GB: 4.4 TB/s); 16 rows 16 us.
+// gradient 148 us, weights' gradient behind it 210 us (0.92 GB: 4.4 TB/s; 218 with
+// nothing in the caches); 16 rows 16 us.
 // One workgroup per tile with its own copies took 214, 254 and 440 us.
 #include <type_traits>
 

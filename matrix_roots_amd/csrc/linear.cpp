@@ -13,7 +13,6 @@ using namespace mr;
 namespace {
 
 constexpr int64_t kMaxCols = 65536;
-constexpr int64_t kMaxContraction = int64_t(1) << 30;
 constexpr int64_t kMaxLd = int64_t(1) << 22;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxExperts = 4096;
@@ -270,7 +269,7 @@ mr_status block_scaled_matmul(const mr_scaled_matmul_problem* p, void* ws, size_
   a.c = p->C, a.ldc = p->ldc, a.c_type = p->c_dtype;
   a.partial = static_cast<float*>(need ? ws : nullptr);
   a.m = p->m, a.n = (int32_t)p->n, a.k = (int32_t)p->k;
-  a.p_vector = !b_square, a.p_shift = b_square ? 7 : 0, a.q_shift = a_square ? 7 : 0;
+  a.p_shift = b_square ? 7 : 0, a.q_shift = a_square ? 7 : 0;
   a.fast = units16(p->A, p->lda, 1) && units16(p->B, p->ldb, 1) && (p->k % 16 == 0 || p->padded);
   a.q_e5m2 = p->a_dtype == MR_E5M2;
   a.accumulate = p->accumulate != 0;

@@ -65,7 +65,6 @@ struct ScaledArgs {
   int64_t ldp, ldq, ldsp, ldsq, ldc;
   int64_t m;
   int32_t n, k;
-  int32_t p_vector;        // P's scales: one per row (else per 128 rows)
   int32_t p_shift;         // P's scales: row >> p_shift (0: one per row, 7: per 128 rows)
   int32_t q_shift;         // Q's scales: row >> q_shift (0: one per row, 7: per 128 rows)
   int32_t fast;            // both operands in whole 16-byte units at 16-byte addresses

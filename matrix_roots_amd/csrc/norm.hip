@@ -8,7 +8,7 @@
 //   dx = dres + rho (g - hh mean_j(g_j hh_j)),  g = dy w,  hh = h rho,
 //   dw_j = sum over rows of dy_j hh_j.
 //
-// All sums are float32 (a row's: at most 256 terms per lane, then a tree; a
+// All sums are float32 (a row's: at most 32 terms per lane, then a tree; a
 // column's: one accumulator per lane over the workgroup's rows, the
 // workgroups' sums added in a fixed order, so no result depends on timing).
 //
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_backward_kernel(const 
 
 // dweight[c] = sum over workgroups of their column sums: 32 columns per
 // workgroup, 32 groups of lanes over every 32nd partial row (16 rows each of
-// 512, all loads in flight at once: 6 us for 512 x 2048 sums where one thread
+// 512, all loads in flight at once: 4.6 us for 512 x 2048 sums where one thread
 // per column and four waves took 38), joined in a fixed order.
 __global__ __launch_bounds__(1024) void norm_weight_grad_kernel(const float* partial, int blocks, int width,
                                                                 float* dweight) {

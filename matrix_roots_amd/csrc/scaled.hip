@@ -30,10 +30,12 @@
 // instructions alone take about 130 us (4.3 PFLOP/s with four additions each,
 // registers only); the rest is what they wait for: copies into LDS (64 KB a
 // chunk and CU; 247 us without them), the stores of C (32 us, all CUs at once),
-// and the clock, which falls to 2 GHz.  8192 x 2048 x 16383 to float32: 562 us,
-// 0.98 PFLOP/s, on fp16 instructions (1.5 in the vendor's bf16 product) with the
-// widening and two vector operations per result beside them.  8 x 4096 x 1024:
-// 3.8 us, a launch and one pass over 4 MB.
+// and the clock, which falls to 2 GHz.  8192 x 2048 x 16383 to float32: 555 us,
+// 0.99 PFLOP/s, on fp16 instructions (1.5 in the vendor's bf16 product).  There
+// vector instructions take 45% of a SIMD's cycles (4.4 per matrix instruction:
+// widening, scaling, adding), matrix instructions 41% and LDS 14%; the two waves of
+// a SIMD do little of the first two at the same time.  8 x 4096 x 1024: 3.8 us, a
+// launch and one pass over 4 MB.
 #include <type_traits>
 
 #include "tile_core.hpp"
@@ -773,8 +775,9 @@ ScaledPlan scaled_plan(int64_t m, int64_t n, int64_t k) {
 }
 
 hipError_t launch_scaled(const ScaledArgs& a, const ScaledPlan& plan, hipStream_t s) {
-  if (a.q_e5m2) return a.p_vector ? go_width<1, true>(a, plan.kind, s) : go_width<1, false>(a, plan.kind, s);
-  return a.p_vector ? go_width<0, true>(a, plan.kind, s) : go_width<0, false>(a, plan.kind, s);
+  const bool p_vector = a.p_shift == 0;
+  if (a.q_e5m2) return p_vector ? go_width<1, true>(a, plan.kind, s) : go_width<1, false>(a, plan.kind, s);
+  return p_vector ? go_width<0, true>(a, plan.kind, s) : go_width<0, false>(a, plan.kind, s);
 }
 
 hipError_t launch_scaled_join(const ScaledArgs& a, hipStream_t s) {
