@@ -14,8 +14,8 @@ from matrix_roots_amd import binding as B  # noqa: E402
 U = 2.0 ** -24
 H = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
-# few rows, 128 x 128 tiles, large tiles, a split contraction of few and of more rows
-SIZES = [(8, 300, 256), (300, 264, 384), (4200, 4100, 128), (16, 64, 8192), (130, 100, 4096)]
+# few rows, 128 x 128 tiles, large tiles (one chunk; several, the last one ragged), a split contraction of few and of more rows
+SIZES = [(8, 300, 256), (300, 264, 384), (4200, 4100, 128), (4200, 4100, 400), (16, 64, 8192), (130, 100, 4096)]
 
 
 @pytest.fixture(scope="module")
