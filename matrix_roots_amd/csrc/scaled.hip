@@ -411,18 +411,20 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void scaled_tile_ker
     // are added here, and nothing for them by the common way.  Q's fragments are in registers, P's come from
     // LDS again.  Between the first step and the second, after the sums of all chunks before.
     auto take_in_turn = [&](const unsigned char* st) {
+      // zero rows have the smallest scales: nothing to do for them, unless the product is infinite (a tenth of
+      // the rows zero in e5m2, 1024 x 8192 x 8192: 87 us for 79 without such rows; with the scales first, 94)
+      bool any = false;
+#pragma unroll
+      for (int cb = 0; cb < S::CB; ++cb)
+        any |= !__builtin_amdgcn_classf(sc[cb], 0x108) && (holds_values(fq[cb]) || __builtin_isinf(sc[cb]));
+      if (__ballot(any) == 0) return;
       int l;  // the lane, worked out here: the loops leave no register for what this needs
       asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
       const float* sq = reinterpret_cast<const float*>(st + S::SQ) + qrow + (l & 15);
       const float s = reinterpret_cast<const float*>(st + S::SP)[prow];
-      bool any = false;
 #pragma unroll
-      for (int cb = 0; cb < S::CB; ++cb) {
-        const bool in_turn = BothScales(sq[cb * 16], s).in_turn;
-        any |= in_turn && holds_values(fq[cb]);  // (zero rows have the smallest scales)
-        if (in_turn) sc[cb] = 0.f;
-      }
-      if (__ballot(any) == 0) return;
+      for (int cb = 0; cb < S::CB; ++cb)
+        if (BothScales(sq[cb * 16], s).in_turn) sc[cb] = 0.f;
 #pragma unroll
       for (int cb = 0; cb < S::CB; ++cb) add(0, cb, sc[cb], sr);
 #pragma unroll
