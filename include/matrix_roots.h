@@ -583,6 +583,63 @@ size_t rms_norm_backward_workspace(const mr_rms_norm_grad_problem* problem);
 mr_status rms_norm_backward(const mr_rms_norm_grad_problem* problem, void* ws, size_t ws_bytes, void* hip_stream);
 
 /*
+ * Layer norm of rows, with the residual's addition before it and an 8-bit output
+ * after it:
+ *   h = x + residual, rounded to dtype (h = x without a residual),
+ *   mean_i = mean_j h_ij,  rstd_i = (mean_j (h_ij - mean_i)^2 + eps)^(-1/2),
+ *   y_ij = (h_ij - mean_i) rstd_i weight_j + bias_j,
+ *   scales and q from the float32 y as rms_norm_forward's.
+ * width in [1, 16384].  dtype (x, residual, h, y): MR_F32, MR_F16 or MR_BF16;
+ * w_dtype (weight, bias): dtype or MR_F32.  bias may be NULL (none).  h is
+ * required with a residual and ignored without one; mean, rstd, y and q (with
+ * scales, MR_BLOCK_VECTOR) are each written where not NULL, at least one of y
+ * and q.
+ */
+typedef struct {
+  int64_t rows, width;
+  const void* x;        int64_t ldx;
+  const void* residual; int64_t ldres;
+  const void* weight;
+  const void* bias;
+  void* h;              int64_t ldh;
+  float* mean;
+  float* rstd;
+  void* y;              int64_t ldy;
+  void* q;              int64_t ldq;
+  float* scales;        int64_t lds;
+  mr_dtype dtype, w_dtype, q_dtype;
+  int32_t reserved;
+  double eps;
+} mr_layer_norm_problem;
+mr_status layer_norm_forward(const mr_layer_norm_problem* problem, void* hip_stream);
+
+/*
+ * Gradient of layer_norm_forward from dy, the gradient of y:
+ *   xh = (h - mean) rstd,  g = dy weight,
+ *   dx = dresidual + rstd (g - mean_j(g) - xh mean_j(g xh)),
+ *   dweight_j = sum_i dy_ij xh_ij,  dbias_j = sum_i dy_ij (float32).
+ * h, mean and rstd as the forward pass left them.  dresidual: the gradient that
+ * reaches h by the residual path, or NULL.  dweight and dbias may each be NULL.
+ * Workspace: layer_norm_backward_workspace bytes, 256-byte aligned (0 when both
+ * are NULL).
+ */
+typedef struct {
+  int64_t rows, width;
+  const void* dy;        int64_t lddy;
+  const void* h;         int64_t ldh;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  const void* dresidual; int64_t ldres;
+  void* dx;              int64_t lddx;
+  float* dweight;
+  float* dbias;
+  mr_dtype dtype, w_dtype;
+} mr_layer_norm_grad_problem;
+size_t layer_norm_backward_workspace(const mr_layer_norm_grad_problem* problem);
+mr_status layer_norm_backward(const mr_layer_norm_grad_problem* problem, void* ws, size_t ws_bytes, void* hip_stream);
+
+/*
  * Quantises X (m x n; x_dtype MR_F32, MR_F16 or MR_BF16) to q_dtype (MR_E4M3 or
  * MR_E5M2) with scales and quotients as rms_norm_forward's, in one reading of X:
  *   Q (m x n) with scales S, blocks along n, and/or
@@ -680,6 +737,137 @@ typedef struct {
   int32_t offset_bits, accumulate;
 } mr_grouped_grad_problem;
 mr_status grouped_weight_grad(const mr_grouped_grad_problem* problem, void* hip_stream);
+
+/*
+ * ---- Around a bank of experts ----
+ *
+ * From the logits of a router to the rows that the grouped products take, and
+ * back.  The conventions of the linear-layer operators hold; `chosen`,
+ * `weights`, `place` and their gradients are contiguous arrays of tokens x k.
+ *
+ * Chooses k experts for each token: the largest logits l, in that order, ties to
+ * the lowest index.  -inf is never chosen; where fewer than k are left, `chosen`
+ * is -1 and the weight 0.  With S all experts (normalize 0) or the chosen (1):
+ *   log_sum = log sum_{e in S} exp(l_e),  weight_j = exp(l_{chosen_j} - log_sum),
+ * log_sum -inf for a token without experts.  NaN counts as the largest; a row
+ * that holds one, or +inf, gets experts and NaN weights.  experts in [1, 4096],
+ * k in [1, min(16, experts)].
+ */
+typedef struct {
+  int64_t tokens, experts, k;
+  const void* logits; int64_t ldl;
+  int32_t* chosen;
+  float* weights;
+  float* log_sum; /* tokens */
+  mr_dtype dtype; /* of the logits: MR_F32, MR_F16 or MR_BF16 */
+  int32_t normalize;
+} mr_route_problem;
+mr_status route_tokens(const mr_route_problem* problem, void* hip_stream);
+
+/*
+ * Gradient of the logits (tokens x experts, dtype) from dweights, with c = sum_j
+ * weight_j dweight_j over a token's chosen:
+ *   normalize 1: weight_j (dweight_j - c) at the chosen, 0 elsewhere,
+ *   normalize 0: weight_j dweight_j at the chosen, less softmax(l)_e c everywhere.
+ * chosen and weights as route_tokens left them; choices of -1 (or of any other
+ * number that is no expert) have no part in it.  logits are read with normalize 0
+ * only.
+ */
+typedef struct {
+  int64_t tokens, experts, k;
+  const void* logits; int64_t ldl;
+  const int32_t* chosen;
+  const float* weights;
+  const float* dweights;
+  void* dlogits;      int64_t ldd;
+  mr_dtype dtype;
+  int32_t normalize;
+} mr_route_grad_problem;
+mr_status route_tokens_backward(const mr_route_grad_problem* problem, void* hip_stream);
+
+/*
+ * Sorts the tokens' choices (device integers of index_bits 32 or 64 bits, tokens
+ * x k in rows ldc apart) by expert, choices of one expert by token and place:
+ *   offsets[e] .. offsets[e + 1] - 1: the sorted rows of expert e (experts + 1
+ *   values, as the grouped products take them),
+ *   place[t k + j]: the sorted row of choice j of token t.
+ * Choices of no expert (a number outside 0 .. experts - 1) come last, from
+ * offsets[experts] on, so the places are a permutation of 0 .. tokens k - 1.
+ * experts in [1, 4096], k in [1, 64], tokens k < 2^31.  Workspace:
+ * order_by_expert_workspace bytes (0 for up to 16384 choices), 256-byte aligned.
+ */
+typedef struct {
+  int64_t tokens, experts, k;
+  const void* chosen; int64_t ldc;
+  int32_t* offsets;
+  int32_t* place;
+  int32_t index_bits, reserved;
+} mr_order_problem;
+size_t order_by_expert_workspace(const mr_order_problem* problem);
+mr_status order_by_expert(const mr_order_problem* problem, void* ws, size_t ws_bytes, void* hip_stream);
+
+/*
+ * A token's row of X (tokens x width) to the sorted rows of its choices, Y
+ * (tokens k x width): Y[place_tj] = weight_tj X_t (weights NULL: X_t), zeros in
+ * the rows of no expert (from offsets[experts] on).  With Z (rows like Y's), also
+ *   dots_tj = <Z[place_tj], X_t> (float32; 0 for rows of no expert, whose Z is not read).
+ * With weights, Z and dots this is the gradient of combine_rows: X its output's
+ * gradient, Y that of its rows, dots that of its weights.  weights need Z and
+ * dots.  Places that are no row are left out.
+ */
+typedef struct {
+  int64_t tokens, experts, k, width;
+  const void* X; int64_t ldx;
+  const int32_t* place;
+  const int32_t* offsets;
+  const float* weights;
+  const void* Z; int64_t ldz;
+  void* Y;       int64_t ldy;
+  float* dots;
+  mr_dtype dtype; /* of X, Y and Z: MR_F32, MR_F16 or MR_BF16 */
+  int32_t reserved;
+} mr_dispatch_problem;
+mr_status dispatch_rows(const mr_dispatch_problem* problem, void* hip_stream);
+
+/*
+ * The sorted rows Y (tokens k x width) of a token's choices added up, in float32
+ * and in the choices' order:
+ *   OUT_t = residual_t + sum_j weight_tj Y[place_tj]
+ * (weights NULL: 1, residual NULL: 0), over the choices that an expert has.
+ * Without weights and residual this is the gradient of dispatch_rows.
+ */
+typedef struct {
+  int64_t tokens, experts, k, width;
+  const void* Y;        int64_t ldy;
+  const int32_t* place;
+  const int32_t* offsets;
+  const float* weights;
+  const void* residual; int64_t ldres;
+  void* OUT;            int64_t ldo;
+  mr_dtype dtype; /* of Y, residual and OUT */
+  int32_t reserved;
+} mr_combine_problem;
+mr_status combine_rows(const mr_combine_problem* problem, void* hip_stream);
+
+/*
+ * Clips gradients by their common norm: with n_i = ||G_i||_F, n = (sum n_i^2)^(1/2),
+ *   OUT_i = G_i max_norm / n  where n is finite and larger than max_norm,
+ *   OUT_i = G_i               else (a norm that is not finite is for the caller to see).
+ * OUT NULL: in place (then nothing is written where nothing changes).  Sums and
+ * the factor are float64.  norms_dev: count + 1 device doubles, n and then every
+ * n_i.  max_norm INFINITY: the norms alone.  m and n may be 0, up to 2^40 values
+ * each.  dtype: MR_F32, MR_F16 or MR_BF16; out_dtype: dtype or MR_F32.
+ * Workspace: clip_gradients_batched_workspace bytes, 256-byte aligned.
+ */
+typedef struct {
+  int64_t m, n;
+  void* G;   int64_t ldg;
+  void* OUT; int64_t ldo;
+  mr_dtype dtype, out_dtype;
+} mr_clip_problem;
+size_t clip_gradients_batched_workspace(const mr_clip_problem* problems, int32_t count);
+mr_status clip_gradients_batched(const mr_clip_problem* problems, int32_t count, double max_norm, double* norms_dev,
+                                 void* ws, size_t ws_bytes, void* hip_stream);
 
 const char* mr_status_string(mr_status status);
 const char* mr_last_error_message(void);

@@ -52,11 +52,22 @@ EXPORTED = (
     "rms_norm_forward",
     "rms_norm_backward",
     "rms_norm_backward_workspace",
+    "layer_norm_forward",
+    "layer_norm_backward",
+    "layer_norm_backward_workspace",
     "quantize_blocks",
     "block_scaled_matmul",
     "block_scaled_matmul_workspace",
     "grouped_matmul",
     "grouped_weight_grad",
+    "route_tokens",
+    "route_tokens_backward",
+    "order_by_expert",
+    "order_by_expert_workspace",
+    "dispatch_rows",
+    "combine_rows",
+    "clip_gradients_batched",
+    "clip_gradients_batched_workspace",
     "mr_newton_iterations",
     "mr_newton_schedule",
     "mr_measure_peaks",
@@ -117,6 +128,24 @@ class RmsNormGradProblem(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32)]
 
 
+class LayerNormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldres", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
+class LayerNormGradProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("ldres", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
+
+
 class QuantizeProblem(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64),
                 ("Q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("S", ctypes.c_void_p), ("lds", ctypes.c_int64),
@@ -148,6 +177,49 @@ class GroupedGradProblem(ctypes.Structure):
                 ("offsets", ctypes.c_void_p), ("DW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
                 ("dw_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
                 ("offset_bits", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class RouteProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("ldl", ctypes.c_int64), ("chosen", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("log_sum", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("normalize", ctypes.c_int32)]
+
+
+class RouteGradProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("ldl", ctypes.c_int64), ("chosen", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("dweights", ctypes.c_void_p),
+                ("dlogits", ctypes.c_void_p), ("ldd", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("normalize", ctypes.c_int32)]
+
+
+class OrderProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("chosen", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("place", ctypes.c_void_p), ("index_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class DispatchProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("place", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("Z", ctypes.c_void_p),
+                ("ldz", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("dots", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CombineProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("place", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ldres", ctypes.c_int64), ("OUT", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ClipProblem(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("G", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("OUT", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 ROOT_INFO_DTYPE = np.dtype([("scale", "<f8"), ("bound", "<f8"), ("iters", "<i4"), ("fp64_iters", "<i4"),
@@ -217,6 +289,12 @@ def library() -> ctypes.CDLL:
     lib.rms_norm_backward.restype = i32
     lib.rms_norm_backward_workspace.argtypes = [vp]
     lib.rms_norm_backward_workspace.restype = sz
+    lib.layer_norm_forward.argtypes = [vp, vp]
+    lib.layer_norm_forward.restype = i32
+    lib.layer_norm_backward.argtypes = [vp, vp, sz, vp]
+    lib.layer_norm_backward.restype = i32
+    lib.layer_norm_backward_workspace.argtypes = [vp]
+    lib.layer_norm_backward_workspace.restype = sz
     lib.quantize_blocks.argtypes = [vp, vp]
     lib.quantize_blocks.restype = i32
     lib.block_scaled_matmul.argtypes = [vp, vp, sz, vp]
@@ -227,6 +305,22 @@ def library() -> ctypes.CDLL:
     lib.grouped_matmul.restype = i32
     lib.grouped_weight_grad.argtypes = [vp, vp]
     lib.grouped_weight_grad.restype = i32
+    lib.route_tokens.argtypes = [vp, vp]
+    lib.route_tokens.restype = i32
+    lib.route_tokens_backward.argtypes = [vp, vp]
+    lib.route_tokens_backward.restype = i32
+    lib.order_by_expert.argtypes = [vp, vp, sz, vp]
+    lib.order_by_expert.restype = i32
+    lib.order_by_expert_workspace.argtypes = [vp]
+    lib.order_by_expert_workspace.restype = sz
+    lib.dispatch_rows.argtypes = [vp, vp]
+    lib.dispatch_rows.restype = i32
+    lib.combine_rows.argtypes = [vp, vp]
+    lib.combine_rows.restype = i32
+    lib.clip_gradients_batched.argtypes = [vp, i32, f64, vp, vp, sz, vp]
+    lib.clip_gradients_batched.restype = i32
+    lib.clip_gradients_batched_workspace.argtypes = [vp, i32]
+    lib.clip_gradients_batched_workspace.restype = sz
     lib.mr_newton_iterations.argtypes = [i32, f64, f64]
     lib.mr_newton_iterations.restype = i32
     lib.mr_newton_schedule.argtypes = [f64, vp, i32, vp, vp]
@@ -601,6 +695,86 @@ def hyperball_update_batched(Ws: Sequence, Us: Sequence, lr: float, return_norms
     _check(lib.hyperball_update_batched(ctypes.addressof(probs), count, float(lr), _ptr(norms), _ptr(ws), need,
                                         _stream(stream)))
     return norms
+
+
+def _rows_of(t):
+    """(m, n, leading dimension) of a tensor's values, in any order, as rows with unit stride: one row where they are
+    dense."""
+    if t.is_contiguous():
+        return 1, t.numel(), 0
+    dims = sorted(((st, n) for st, n in zip(t.stride(), t.shape) if n != 1), reverse=True)
+    if t.numel() == 0:
+        return 1, 0, 0
+    if dims[-1][0] != 1:
+        raise ValueError("gradients need a dimension of unit stride")
+    m, n, ld = 1, 1, 0
+    for st, size in reversed(dims):  # from the innermost out
+        if m == 1 and st == n:
+            n *= size
+        elif m == 1 and st > n:
+            m, ld = size, st
+        elif m > 1 and st == m * ld:
+            m *= size
+        else:
+            raise ValueError("gradients must be rows one stride apart")
+    return m, n, ld
+
+
+def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequence] = None,
+                           return_norms: bool = False, stream=None):
+    """Scales the gradients by max_norm / n where their common norm n is finite and
+    larger than max_norm; in place, or into `outs`, which hold the gradients in
+    either case then.
+
+    grads: float32, float16 or bfloat16 device tensors of any shape whose values
+    lie in rows one stride apart; outs: tensors of the same shapes and strides'
+    order, of the gradient's type or float32 (as gram_ema_update takes them).
+    Returns n, a float64 device scalar; with return_norms (n, norms), the
+    gradients' own norms.  max_norm math.inf: the norms alone.
+    """
+    import torch
+
+    codes = {torch.float32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
+    lib = library()
+    count = len(grads)
+    if count == 0:
+        raise ValueError("no gradients")
+    if outs is not None and len(outs) != count:
+        raise ValueError("one output per gradient")
+    dev = grads[0].device
+    probs = (ClipProblem * count)()
+    for i, g in enumerate(grads):
+        code = codes.get(g.dtype)
+        if code is None:
+            raise ValueError(f"gradient {i} is {g.dtype}: float32, float16 or bfloat16 is needed")
+        if g.device != dev:
+            raise ValueError("all gradients must be on one device")
+        if outs is None:
+            m, n, ld = _rows_of(g)
+            probs[i] = ClipProblem(m, n, g.data_ptr(), ld, 0, 0, code, code)
+            continue
+        o = outs[i]
+        if o.shape != g.shape or o.device != dev:
+            raise ValueError(f"output {i} does not match its gradient")
+        if o.dtype != g.dtype and o.dtype != torch.float32:
+            raise ValueError(f"output {i} is {o.dtype}: the gradient's type or float32 is needed")
+        if g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride():
+            m, n, ld = _rows_of(g)
+            ldo = ld
+        elif g.dim() == 2 and g.stride(1) == 1 and o.stride(1) == 1:
+            (m, n), ld, ldo = g.shape, g.stride(0), o.stride(0)
+        else:
+            raise ValueError(f"output {i} must lie as its gradient does")
+        probs[i] = ClipProblem(m, n, g.data_ptr(), ld, o.data_ptr(), ldo, code, codes[o.dtype])
+    need = lib.clip_gradients_batched_workspace(ctypes.addressof(probs), count)
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
+        norms = torch.empty(count + 1, dtype=torch.float64, device=dev)
+    _in_use_here(stream, norms)
+    _in_use_on(stream, ws, norms)
+    _check(lib.clip_gradients_batched(ctypes.addressof(probs), count, float(max_norm), _ptr(norms), _ptr(ws), need,
+                                      _stream(stream)))
+    return (norms[0], norms[1:]) if return_norms else norms[0]
 
 
 def cans_ceilings():

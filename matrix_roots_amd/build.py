@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmatrix_roots.so")
 SOURCES = ["abi.cpp", "gram.hip", "apply.hip", "root.hip", "jacobi.hip", "cans.hip", "polar.hip", "step.hip",
-           "peaks.hip", "linear.cpp", "norm.hip", "quantize.hip", "scaled.hip", "grouped.hip"]
+           "peaks.hip", "linear.cpp", "norm.hip", "quantize.hip", "scaled.hip", "grouped.hip",
+           "layer_norm.hip", "experts.cpp", "routing.hip", "clip.hip"]
 ARCH = "gfx950"
 
 # Packed float32 VALU ops are kept out of every code object.

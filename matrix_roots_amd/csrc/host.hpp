@@ -110,7 +110,9 @@ enum TraceClass {
   kTrFinalize, kTrInfo, kTrNewtonX3, kTrCansBound, kTrCansInit, kTrCansP, kTrCansYZ, kTrCansFinal, kTrCansInfo,
   kTrPolarStats, kTrPolarBound, kTrPolarInit, kTrPolarA, kTrPolarX, kTrPolarFinal, kTrPolarInfo,
   kTrMomentum, kTrHyperReduce, kTrHyperUpdate, kTrApplyX3, kTrApplySplit, kTrSlice, kTrNewtonI8, kTrMoment,
-  kTrNorm, kTrNormGrad, kTrQuantize, kTrScaledMatmul, kTrGrouped, kTrGroupedGrad, kTrCount
+  kTrNorm, kTrNormGrad, kTrQuantize, kTrScaledMatmul, kTrGrouped, kTrGroupedGrad,
+  kTrLayerNorm, kTrLayerNormGrad, kTrRoute, kTrRouteGrad, kTrOrder, kTrDispatch, kTrCombine, kTrClipNorm,
+  kTrClipScale, kTrCount
 };
 inline const char* const kTraceNames[kTrCount] = {"syrk_ema", "jacobi", "root_stats", "root_bound",
                                            "root_init", "newton_f64", "newton_f32", "newton_convert",
@@ -121,7 +123,8 @@ inline const char* const kTraceNames[kTrCount] = {"syrk_ema", "jacobi", "root_st
                                            "hyperball_reduce", "hyperball_update", "apply_x3", "apply_split",
                                            "newton_slice", "newton_i8", "root_moment",
                                            "norm", "norm_grad", "quantize", "scaled_matmul", "grouped",
-                                           "grouped_grad"};
+                                           "grouped_grad", "layer_norm", "layer_norm_grad", "route", "route_grad",
+                                           "expert_order", "dispatch", "combine", "clip_norm", "clip_scale"};
 struct TraceEntry {
   int cls;
   hipEvent_t a, b;

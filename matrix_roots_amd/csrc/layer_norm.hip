@@ -1,0 +1,289 @@
+// Layer norm of rows, with the residual's addition before it and an 8-bit
+// output with a scale per 128 columns after it, and its gradient:
+//
+//   h = x + r (rounded to the stored type), mu = mean_j h_j,
+//   rho = (mean_j (h_j - mu)^2 + eps)^(-1/2),  y_j = (h_j - mu) rho w_j + b_j,
+//   and y in 8 bits as the root-mean-square norm's;
+//
+//   dx = dres + rho (g - mean_j g_j - hh mean_j(g_j hh_j)),  g = dy w,
+//   hh = (h - mu) rho,  dw_j = sum over rows of dy_j hh_j,  db_j = of dy_j.
+//
+// A row stays in registers from its loads to its last output, so the mean is
+// known before the squares are added: with m the rounded mean and d = h - m,
+// mu = m + mean(d) and the variance is mean(d^2) - mean(d)^2.  mean(d) is what
+// m was rounded by; without it a row of equal values far from zero would come
+// out as that rounding over sqrt(eps).  Sums are float32 in an order that sizes
+// alone decide.
+#include "mr_common.hpp"
+#include "norm_common.hpp"
+
+namespace mr {
+
+namespace {
+
+// Sums of two values over the row's threads, in each of them.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& u, float& v, float (*red)[16]) {
+  u = sum64(u);
+  v = sum64(v);
+  if constexpr (TPR == 64) return;
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[0][wave] = u, red[1][wave] = v;
+  __syncthreads();
+  u = red[0][0], v = red[1][0];
+#pragma unroll
+  for (int w = 1; w < TPR / 64; ++w) u += red[0][w], v += red[1][w];
+}
+
+}  // namespace
+
+template <typename T, int TPR, int CH>
+__global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(const LayerNormArgs a) {
+  __shared__ float red[2][16];
+  constexpr int RPB = kNormThreads<TPR> / TPR, NV = 8;
+  int t = RPB == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;  // place among the row's threads
+  const float inv_width = 1.f / (float)a.width;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t r = RPB == 1 ? r0 : r0 + threadIdx.x / TPR;
+    asm volatile("" : "+v"(t));  // columns and addresses are worked out per row, not kept in registers over the loop
+    if (TPR == 64 && r >= a.rows) break;  // whole waves: no barrier follows
+    const T* x = reinterpret_cast<const T*>(a.x) + r * a.ldx;
+    const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
+    float v[CH][NV];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) load_chunk<T>(x, chunk_col<TPR>(t, k), a.width, v[k]);
+    if (res) {
+      T* h = reinterpret_cast<T*>(a.h) + r * a.ldh;
+      float u[CH][NV];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) load_chunk<T>(res, chunk_col<TPR>(t, k), a.width, u[k]);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        // the stored sum, rounded to T, is what the norm is of: the backward pass reads it
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[k][i] = widen(narrow<T>(v[k][i] + u[k][i]));
+        store_chunk<T>(h, chunk_col<TPR>(t, k), a.width, v[k]);
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s += v[k][i];
+    const float m = row_sum<TPR>(s, red[0]) * inv_width;
+    float ds = 0.f, ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = chunk_col<TPR>(t, k);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[k][i] = c + i < a.width ? v[k][i] - m : 0.f;
+        ds += v[k][i];
+        ss = fmaf(v[k][i], v[k][i], ss);
+      }
+    }
+    row_sum2<TPR>(ds, ss, red);
+    const float e = ds * inv_width;
+    const float rho = 1.f / sqrtf(fmaxf(fmaf(-e, e, ss * inv_width), 0.f) + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[r] = m + e;
+      if (a.rstd) a.rstd[r] = rho;
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int c = chunk_col<TPR>(t, k);
+      float w[NV], b[NV];
+      load_param<T>(a.w, a.w_f32, c, a.width, w);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) b[i] = 0.f;
+      if (a.b) load_param<T>(a.b, a.w_f32, c, a.width, b);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[k][i] = fmaf((v[k][i] - e) * rho, w[i], b[i]);
+      if (a.y) store_chunk<T>(reinterpret_cast<T*>(a.y) + r * a.ldy, c, a.width, v[k]);
+      if (a.q) store_eight(a.q + r * a.ldq, a.s + r * a.lds, c, a.width, v[k], a.e5m2);  // 0 behind the row's end
+    }
+  }
+}
+
+// Rows r0, r0 + gridDim RPB, ...: dx, and this workgroup's column sums of dy hh
+// and of dy into a.partial[2 blockIdx.x] and the row behind it.
+template <typename T, int TPR, int CH>
+__global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(const LayerNormArgs a) {
+  constexpr int RPB = kNormThreads<TPR> / TPR, NV = 8;
+  __shared__ float red[2][16];
+  __shared__ float cols[RPB > 1 ? 2 * TPR * CH * NV : 1];
+  int t = RPB == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;  // place among the row's threads
+  const float inv_width = 1.f / (float)a.width;
+  float dw[CH][NV], db[CH][NV];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) dw[k][i] = db[k][i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t r = RPB == 1 ? r0 : r0 + threadIdx.x / TPR;
+    asm volatile("" : "+v"(t));  // columns and addresses are worked out per row, not kept in registers over the loop
+    if (TPR == 64 && r >= a.rows) break;  // whole waves: the barriers below come after the loop
+    const T* dy = reinterpret_cast<const T*>(a.dy) + r * a.lddy;
+    const T* h = reinterpret_cast<const T*>(a.x) + r * a.ldx;
+    const float rho = a.rstd_in[r], mu = a.mean_in[r];
+    float g[CH][NV], hh[CH][NV];
+    float sg = 0.f, dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      load_chunk<T>(dy, chunk_col<TPR>(t, k), a.width, g[k]);
+      load_chunk<T>(h, chunk_col<TPR>(t, k), a.width, hh[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      float w[NV];
+      load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        hh[k][i] = (hh[k][i] - mu) * rho;
+        dw[k][i] = fmaf(g[k][i], hh[k][i], dw[k][i]);
+        db[k][i] += g[k][i];
+        g[k][i] *= w[i];  // 0 behind the row's end
+        sg += g[k][i];
+        dot = fmaf(g[k][i], hh[k][i], dot);
+      }
+    }
+    // under way during the reduction
+    const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
+    Raw8<T> rr[CH];
+    if (res) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int col = chunk_col<TPR>(t, k);
+        if (col + 8 <= a.width) rr[k] = load8<T>(res + col);
+      }
+    }
+    row_sum2<TPR>(sg, dot, red);
+    const float c0 = sg * inv_width, c1 = dot * inv_width;
+    T* dx = reinterpret_cast<T*>(a.y) + r * a.ldy;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      float u[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) u[i] = 0.f;
+      if (res) {
+        const int col = chunk_col<TPR>(t, k);
+        if (col + 8 <= a.width)
+          widen8(rr[k], u);
+        else
+          load_chunk<T>(res, col, a.width, u);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) u[i] += rho * (g[k][i] - c0 - hh[k][i] * c1);
+      store_chunk<T>(dx, chunk_col<TPR>(t, k), a.width, u);
+    }
+  }
+  if (!a.partial) return;
+  float* out = a.partial + 2 * (int64_t)blockIdx.x * a.width;
+  if constexpr (RPB > 1) {
+    constexpr int B = TPR * CH * NV;
+    for (int w = 1; w < RPB; ++w) {  // waves 1, 2, 3 add to wave 0's sums in turn
+      if ((int)threadIdx.x / TPR == w) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) cols[(k * NV + i) * TPR + t] = dw[k][i], cols[B + (k * NV + i) * TPR + t] = db[k][i];
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < TPR) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) dw[k][i] += cols[(k * NV + i) * TPR + t], db[k][i] += cols[B + (k * NV + i) * TPR + t];
+      }
+      __syncthreads();
+    }
+    if ((int)threadIdx.x >= TPR) return;
+  }
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    store_chunk<float>(out, chunk_col<TPR>(t, k), a.width, dw[k]);
+    store_chunk<float>(out + a.width, chunk_col<TPR>(t, k), a.width, db[k]);
+  }
+}
+
+// dweight and dbias from the workgroups' sums: 32 of the 2 width columns per
+// workgroup, 32 groups of lanes over every 32nd row, joined in a fixed order.
+__global__ __launch_bounds__(1024) void layer_norm_join_kernel(const float* partial, int blocks, int width,
+                                                               float* dweight, float* dbias) {
+  __shared__ float part[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  float s = 0.f;
+  if (c < 2 * width) {
+#pragma unroll 16
+    for (int b = g; b < blocks; b += 32) s += partial[(int64_t)b * 2 * width + c];
+  }
+  part[g][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (g == 0 && c < 2 * width) {
+    float t = part[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) t += part[i][threadIdx.x];
+    if (c < width) {
+      if (dweight) dweight[c] = t;
+    } else if (dbias) {
+      dbias[c - width] = t;
+    }
+  }
+}
+
+// ------------------------------------------------------------ launchers
+namespace {
+
+constexpr int kMaxBlocks = 2048;  // 8 workgroups per CU
+
+template <typename T, int TPR, int CH>
+hipError_t go(const LayerNormArgs& a, bool backward, int blocks, hipStream_t s) {
+  if (backward)
+    hipLaunchKernelGGL((layer_norm_backward_kernel<T, TPR, CH>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
+  else
+    hipLaunchKernelGGL((layer_norm_forward_kernel<T, TPR, CH>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t pick(const LayerNormArgs& a, bool backward, int blocks, hipStream_t s) {
+  const int w = a.width;
+  if (w <= 512) return go<T, 64, 1>(a, backward, blocks, s);
+  if (w <= 1024) return go<T, 64, 2>(a, backward, blocks, s);
+  if (w <= 2048) return go<T, 64, 4>(a, backward, blocks, s);
+  if (w <= 4096) return go<T, 256, 2>(a, backward, blocks, s);
+  if (w <= 8192) return go<T, 256, 4>(a, backward, blocks, s);
+  return go<T, 512, 4>(a, backward, blocks, s);
+}
+
+hipError_t pick_type(const LayerNormArgs& a, mr_dtype dt, bool backward, int blocks, hipStream_t s) {
+  if (dt == MR_F32) return pick<float>(a, backward, blocks, s);
+  if (dt == MR_F16) return pick<_Float16>(a, backward, blocks, s);
+  return pick<bf16_t>(a, backward, blocks, s);
+}
+
+int64_t row_groups(int64_t rows, int64_t width) { return width <= 2048 ? (rows + 3) / 4 : rows; }
+
+}  // namespace
+
+hipError_t launch_layer_norm_forward(const LayerNormArgs& a, mr_dtype dt, hipStream_t s) {
+  const int64_t g = row_groups(a.rows, a.width);
+  return pick_type(a, dt, false, (int)(g < kMaxBlocks ? g : kMaxBlocks), s);
+}
+
+int layer_norm_backward_blocks(int64_t rows, int64_t width) {
+  const int64_t g = row_groups(rows, width);
+  return (int)(g < 512 ? g : 512);
+}
+
+hipError_t launch_layer_norm_backward(const LayerNormArgs& a, mr_dtype dt, int blocks, hipStream_t s) {
+  return pick_type(a, dt, true, blocks, s);
+}
+
+hipError_t launch_layer_norm_join(const float* partial, int blocks, int width, float* dweight, float* dbias, hipStream_t s) {
+  hipLaunchKernelGGL(layer_norm_join_kernel, dim3((2 * width + 31) / 32), dim3(1024), 0, s, partial, blocks, width, dweight, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace mr

@@ -5,69 +5,9 @@
 #include <cmath>
 #include <cstring>
 
-#include "host.hpp"
-#include "linear.hpp"
+#include "linear_host.hpp"
 
 using namespace mr;
-
-namespace {
-
-constexpr int64_t kMaxCols = 65536;
-constexpr int64_t kMaxLd = int64_t(1) << 22;
-constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int64_t kMaxExperts = 4096;
-
-bool is_float(mr_dtype t) { return t == MR_F32 || t == MR_F16 || t == MR_BF16; }
-bool is_half(mr_dtype t) { return t == MR_F16 || t == MR_BF16; }
-bool is_eight(mr_dtype t) { return t == MR_E4M3 || t == MR_E5M2; }
-size_t size_of(mr_dtype t) { return t == MR_F32 ? 4 : is_half(t) ? 2 : 1; }
-int64_t blocks128(int64_t n) { return (n + kBlock - 1) / kBlock; }
-
-// One matrix argument: present, leading dimension, alignment of its type.
-mr_status check_matrix(const char* name, const void* p, int64_t cols, int64_t ld, size_t es) {
-  if (!p) return fail(MR_ERR_NULL, "%s is NULL", name);
-  if (ld < cols) return fail(MR_ERR_STRIDE, "%s: leading dimension %lld < %lld columns", name, (long long)ld, (long long)cols);
-  if (ld > kMaxLd) return fail(MR_ERR_STRIDE, "%s: leading dimension %lld > %lld", name, (long long)ld, (long long)kMaxLd);
-  if (!aligned(p, es)) return fail(MR_ERR_PARAM, "%s is not aligned to its type", name);
-  return MR_OK;
-}
-mr_status check_size(const char* name, int64_t v, int64_t lo, int64_t hi) {
-  if (v < lo || v > hi)
-    return fail(MR_ERR_SHAPE, "%s %lld outside [%lld, %lld]", name, (long long)v, (long long)lo, (long long)hi);
-  return MR_OK;
-}
-bool units16(const void* p, int64_t ld, size_t es) { return aligned(p, 16) && (ld * (int64_t)es) % 16 == 0; }
-
-#define MR_TRY(x)                            \
-  do {                                       \
-    const mr_status st_ = (x);               \
-    if (st_ != MR_OK) return st_;            \
-  } while (0)
-
-// Alias set whose matrices may have no rows.
-struct Aliases {
-  AliasSet set;
-  void out(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es) {
-    if (p && rows > 0) set.out(range_of(p, rows, cols, ld, es), 0, name);
-  }
-  void in(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es) {
-    if (p && rows > 0) set.in(range_of(p, rows, cols, ld, es), 0, name);
-  }
-};
-
-// The launch's 128 x 128 tiles (with one ragged tile more for each group) fit a grid.
-mr_status check_tiles(int64_t rows, int64_t cols, int64_t groups) {
-  const int64_t t = (blocks128(rows) + groups) * blocks128(cols);
-  return t < (int64_t(1) << 31) ? MR_OK : fail(MR_ERR_SHAPE, "%lld x %lld outputs in one call", (long long)rows, (long long)cols);
-}
-
-mr_status check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (need && (!ws || bytes < need || !aligned(ws, 256)))
-    return fail(MR_ERR_WORKSPACE, "workspace %p of %zu bytes; need %zu bytes, 256-byte aligned", ws, bytes, need);
-  return MR_OK;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -178,6 +118,121 @@ mr_status rms_norm_backward(const mr_rms_norm_grad_problem* p, void* ws, size_t 
   if (!p->dweight) return MR_OK;
   return traced(kTrNormGrad, true, s, [&] { return launch_norm_weight_grad(partial, blocks, (int)w, p->dweight, s); },
                 "norm weight gradient launch");
+}
+
+// ------------------------------------------------------------ layer norm
+mr_status layer_norm_forward(const mr_layer_norm_problem* p, void* hip_stream) {
+  if (!p) return fail(MR_ERR_NULL, "problem is NULL");
+  MR_TRY(check_size("rows", p->rows, 0, kMaxRows));
+  MR_TRY(check_size("width", p->width, 1, kNormMaxWidth));
+  if (!is_float(p->dtype)) return fail(MR_ERR_PARAM, "dtype %d", p->dtype);
+  if (p->w_dtype != p->dtype && p->w_dtype != MR_F32) return fail(MR_ERR_PARAM, "w_dtype %d", p->w_dtype);
+  if (!(p->eps >= 0.0) || !std::isfinite(p->eps)) return fail(MR_ERR_PARAM, "eps %g must be >= 0 and finite", p->eps);
+  if (p->rows > 0 && !p->y && !p->q) return fail(MR_ERR_NULL, "y and q are both NULL");
+  if (!p->weight) return fail(MR_ERR_NULL, "weight is NULL");
+  if (p->q && !is_eight(p->q_dtype)) return fail(MR_ERR_PARAM, "q_dtype %d", p->q_dtype);
+  const size_t es = size_of(p->dtype), ws = size_of(p->w_dtype);
+  if (!aligned(p->weight, ws) || !aligned(p->bias, ws)) return fail(MR_ERR_PARAM, "weight or bias is not aligned to its type");
+  if (!aligned(p->mean, 4) || !aligned(p->rstd, 4)) return fail(MR_ERR_PARAM, "mean or rstd is not aligned to its type");
+  const int64_t w = p->width, nb = blocks128(w);
+  if (p->rows == 0) return MR_OK;
+  MR_TRY(check_matrix("x", p->x, w, p->ldx, es));
+  if (p->residual) {
+    MR_TRY(check_matrix("residual", p->residual, w, p->ldres, es));
+    MR_TRY(check_matrix("h", p->h, w, p->ldh, es));
+  }
+  if (p->y) MR_TRY(check_matrix("y", p->y, w, p->ldy, es));
+  if (p->q) {
+    MR_TRY(check_matrix("q", p->q, w, p->ldq, 1));
+    MR_TRY(check_matrix("scales", p->scales, nb, p->lds, 4));
+  }
+  Aliases al;
+  al.in("x", p->x, p->rows, w, p->ldx, es);
+  al.in("residual", p->residual, p->rows, w, p->ldres, es);
+  al.in("weight", p->weight, 1, w, w, ws);
+  al.in("bias", p->bias, 1, w, w, ws);
+  if (p->residual) al.out("h", p->h, p->rows, w, p->ldh, es);
+  al.out("mean", p->mean, 1, p->rows, p->rows, 4);
+  al.out("rstd", p->rstd, 1, p->rows, p->rows, 4);
+  al.out("y", p->y, p->rows, w, p->ldy, es);
+  al.out("q", p->q, p->rows, w, p->ldq, 1);
+  if (p->q) al.out("scales", p->scales, p->rows, nb, p->lds, 4);
+  MR_TRY(al.set.check());
+  LayerNormArgs a;
+  memset(&a, 0, sizeof a);
+  a.x = p->x, a.ldx = p->ldx;
+  a.res = p->residual, a.ldres = p->ldres;
+  a.w = p->weight, a.b = p->bias, a.w_f32 = p->w_dtype == MR_F32;
+  a.h = p->h, a.ldh = p->ldh;
+  a.mean = p->mean, a.rstd = p->rstd;
+  a.y = p->y, a.ldy = p->ldy;
+  a.q = static_cast<unsigned char*>(p->q), a.ldq = p->ldq;
+  a.s = p->scales, a.lds = p->lds;
+  a.width = (int32_t)w, a.rows = p->rows, a.eps = (float)p->eps, a.e5m2 = p->q_dtype == MR_E5M2;
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  return traced(kTrLayerNorm, true, s, [&] { return launch_layer_norm_forward(a, p->dtype, s); }, "layer norm forward launch");
+}
+
+size_t layer_norm_backward_workspace(const mr_layer_norm_grad_problem* p) {
+  if (!p || (!p->dweight && !p->dbias) || p->rows < 1 || p->rows > kMaxRows || p->width < 1 || p->width > kNormMaxWidth)
+    return 0;
+  return align256((size_t)layer_norm_backward_blocks(p->rows, p->width) * 2 * (size_t)p->width * sizeof(float));
+}
+
+mr_status layer_norm_backward(const mr_layer_norm_grad_problem* p, void* ws, size_t ws_bytes, void* hip_stream) {
+  if (!p) return fail(MR_ERR_NULL, "problem is NULL");
+  MR_TRY(check_size("rows", p->rows, 0, kMaxRows));
+  MR_TRY(check_size("width", p->width, 1, kNormMaxWidth));
+  if (!is_float(p->dtype)) return fail(MR_ERR_PARAM, "dtype %d", p->dtype);
+  if (p->w_dtype != p->dtype && p->w_dtype != MR_F32) return fail(MR_ERR_PARAM, "w_dtype %d", p->w_dtype);
+  if (!p->weight) return fail(MR_ERR_NULL, "weight is NULL");
+  const size_t es = size_of(p->dtype), wes = size_of(p->w_dtype);
+  if (!aligned(p->weight, wes)) return fail(MR_ERR_PARAM, "weight is not aligned to its type");
+  if (!aligned(p->dweight, 4) || !aligned(p->dbias, 4)) return fail(MR_ERR_PARAM, "dweight or dbias is not aligned to its type");
+  const int64_t w = p->width;
+  if (p->rows > 0) {
+    MR_TRY(check_matrix("dy", p->dy, w, p->lddy, es));
+    MR_TRY(check_matrix("h", p->h, w, p->ldh, es));
+    if (!p->mean || !p->rstd) return fail(MR_ERR_NULL, "mean or rstd is NULL");
+    if (!aligned(p->mean, 4) || !aligned(p->rstd, 4)) return fail(MR_ERR_PARAM, "mean or rstd is not aligned to its type");
+    if (p->dresidual) MR_TRY(check_matrix("dresidual", p->dresidual, w, p->ldres, es));
+    MR_TRY(check_matrix("dx", p->dx, w, p->lddx, es));
+  }
+  Aliases al;
+  al.in("dy", p->dy, p->rows, w, p->lddy, es);
+  al.in("h", p->h, p->rows, w, p->ldh, es);
+  if (p->rows) al.in("mean", p->mean, 1, p->rows, p->rows, 4);
+  if (p->rows) al.in("rstd", p->rstd, 1, p->rows, p->rows, 4);
+  al.in("weight", p->weight, 1, w, w, wes);
+  al.in("dresidual", p->dresidual, p->rows, w, p->ldres, es);
+  al.out("dx", p->dx, p->rows, w, p->lddx, es);
+  al.out("dweight", p->dweight, 1, w, w, 4);
+  al.out("dbias", p->dbias, 1, w, w, 4);
+  const size_t need = layer_norm_backward_workspace(p);
+  MR_TRY(check_workspace(ws, ws_bytes, need));
+  if (need) al.out("workspace", ws, 1, (int64_t)need, (int64_t)need, 1);
+  MR_TRY(al.set.check());
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  const int blocks = layer_norm_backward_blocks(p->rows, w);
+  float* partial = static_cast<float*>(need ? ws : nullptr);
+  if (p->rows > 0) {
+    LayerNormArgs a;
+    memset(&a, 0, sizeof a);
+    a.dy = p->dy, a.lddy = p->lddy;
+    a.x = p->h, a.ldx = p->ldh;
+    a.mean_in = p->mean, a.rstd_in = p->rstd;
+    a.w = p->weight, a.w_f32 = p->w_dtype == MR_F32;
+    a.res = p->dresidual, a.ldres = p->ldres;
+    a.y = p->dx, a.ldy = p->lddx;
+    a.partial = partial;
+    a.width = (int32_t)w, a.rows = p->rows;
+    MR_TRY(traced(kTrLayerNormGrad, true, s, [&] { return launch_layer_norm_backward(a, p->dtype, blocks, s); },
+                  "layer norm backward launch"));
+  }
+  if (!p->dweight && !p->dbias) return MR_OK;
+  return traced(kTrLayerNormGrad, true, s,
+                [&] { return launch_layer_norm_join(partial, blocks, (int)w, p->dweight, p->dbias, s); },
+                "layer norm parameters' gradient launch");
 }
 
 // -------------------------------------------------------------- quantise

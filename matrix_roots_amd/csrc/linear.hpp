@@ -39,6 +39,34 @@ hipError_t launch_norm_backward(const NormArgs& a, mr_dtype dt, int blocks, hipS
 hipError_t launch_norm_weight_grad(const float* partial, int blocks, int width, float* dweight, hipStream_t s);
 int norm_backward_blocks(int64_t rows, int64_t width);
 
+struct LayerNormArgs {
+  const void* x;      // backward: h
+  const void* res;    // forward: residual; backward: gradient down the residual (either may be null)
+  const void* w;
+  const void* b;      // may be null
+  const void* dy;     // backward
+  const float* mean_in;
+  const float* rstd_in;
+  void* h;
+  float* mean;
+  float* rstd;
+  void* y;            // backward: dx
+  unsigned char* q;
+  float* s;
+  float* partial;     // backward: two rows of `width` sums per workgroup
+  int64_t ldx, ldres, lddy, ldh, ldy, ldq, lds;
+  int64_t rows;
+  int32_t width;
+  float eps;
+  int32_t w_f32;      // weight and bias are float32 (else of x's type)
+  int32_t e5m2;
+};
+hipError_t launch_layer_norm_forward(const LayerNormArgs& a, mr_dtype dt, hipStream_t s);
+// `blocks` workgroups (layer_norm_backward_blocks), their column sums in a.partial
+hipError_t launch_layer_norm_backward(const LayerNormArgs& a, mr_dtype dt, int blocks, hipStream_t s);
+hipError_t launch_layer_norm_join(const float* partial, int blocks, int width, float* dweight, float* dbias, hipStream_t s);
+int layer_norm_backward_blocks(int64_t rows, int64_t width);
+
 struct QuantArgs {
   const void* x;
   unsigned char* q;

@@ -18,73 +18,10 @@
 // gradient 52 us (268 MB, 5.2 TB/s) and 4.6 us for the columns' join; 1 x 1024:
 // 3.3 us, a launch.  A row belongs to one wave (up to 2048 columns) or to the
 // waves of a workgroup (up to 16384).
-#include "linear_common.hpp"
 #include "mr_common.hpp"
+#include "norm_common.hpp"
 
 namespace mr {
-
-namespace {
-
-// A thread's chunk k of a row: the 8 columns from 8 (t + TPR k), t its place among
-// the row's threads; 16 lanes make a scale block.  The last chunk of a row may
-// be a part of one.
-template <int TPR>
-__device__ __forceinline__ int chunk_col(int t, int k) {
-  return 8 * (t + TPR * k);
-}
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* row, int c, int width, float (&v)[8]) {
-  if (c + 8 <= width) {
-    widen8(load8<T>(row + c), v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if (c < width) {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (c + i < width) v[i] = widen(row[c + i]);
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int c, int width, const float (&v)[8]) {
-  if (c + 8 <= width) {
-    store8<T>(row + c, v);
-  } else if (c < width) {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (c + i < width) row[c + i] = narrow<T>(v[i]);
-  }
-}
-template <typename T>
-__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&v)[8]) {
-  if (a.w_f32)
-    load_chunk<float>(reinterpret_cast<const float*>(a.w), c, a.width, v);
-  else
-    load_chunk<T>(reinterpret_cast<const T*>(a.w), c, a.width, v);
-}
-
-// Sum over the row's threads, in each of them.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = sum64(v);
-  if constexpr (TPR == 64) return v;
-  const int wave = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[wave] = v;
-  __syncthreads();
-  float s = red[0];
-#pragma unroll
-  for (int w = 1; w < TPR / 64; ++w) s += red[w];
-  return s;
-}
-
-}  // namespace
-
-// CH chunks per thread; workgroups of 256 threads (256 / TPR rows at a time) or
-// of TPR.
-template <int TPR>
-constexpr int kNormThreads = TPR < 256 ? 256 : TPR;
 
 template <typename T, int TPR, int CH>
 __global__ __launch_bounds__(kNormThreads<TPR>) void norm_forward_kernel(const NormArgs a) {
@@ -126,31 +63,11 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_forward_kernel(const N
     for (int k = 0; k < CH; ++k) {
       const int c = chunk_col<TPR>(t, k);
       float w[NV];
-      load_weight<T>(a, c, w);
-      uint32_t amax = 0;
+      load_param<T>(a.w, a.w_f32, c, a.width, w);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[k][i] = v[k][i] * rho * w[i];
-        amax = umax(amax, magnitude(v[k][i]));
-      }
+      for (int i = 0; i < NV; ++i) v[k][i] = v[k][i] * rho * w[i];
       if (a.y) store_chunk<T>(reinterpret_cast<T*>(a.y) + r * a.ldy, c, a.width, v[k]);
-      if (a.q) {
-        amax = max16(amax);
-        const float sb = block_scale(amax, a.e5m2);
-        const Quotient over(sb);
-        if (c < a.width && (t & 15) == 0) a.s[r * a.lds + c / kBlock] = sb;
-        unsigned char* q = a.q + r * a.ldq + c;
-        v2u p;
-        p[0] = pack4(over(v[k][0]), over(v[k][1]), over(v[k][2]), over(v[k][3]), a.e5m2);
-        p[1] = pack4(over(v[k][4]), over(v[k][5]), over(v[k][6]), over(v[k][7]), a.e5m2);
-        if (c + 8 <= a.width) {
-          *reinterpret_cast<v2u_any*>(q) = p;
-        } else if (c < a.width) {
-#pragma unroll
-          for (int i = 0; i < 7; ++i)
-            if (c + i < a.width) q[i] = (unsigned char)(p[i >> 2] >> (8 * (i & 3)));
-        }
-      }
+      if (a.q) store_eight(a.q + r * a.ldq, a.s + r * a.lds, c, a.width, v[k], a.e5m2);
     }
   }
 }
@@ -186,7 +103,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void norm_backward_kernel(const 
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float w[NV];
-      load_weight<T>(a, chunk_col<TPR>(t, k), w);
+      load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         hh[k][i] *= rho;

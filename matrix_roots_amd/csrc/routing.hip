@@ -1,0 +1,658 @@
+// What lies between tokens and the products of a bank of experts.
+//
+// Routing: a token's k experts are the k largest of its logits l, ties to the
+// lowest index, -inf never; with S all experts or those k,
+//   log_sum = log sum_{e in S} exp(l_e),  w_j = exp(l_{e_j} - log_sum),
+// and from dw, with c = sum_j w_j dw_j over the chosen,
+//   dl_e = [e chosen] w_e (dw_e - c)            (S the chosen)
+//   dl_e = [e chosen] w_e dw_e - c exp(l_e) / sum_e exp(l_e)   (S all).
+//
+// Order: a stable counting sort of the tokens' choices by expert.  place[t, j] is
+// the row of choice j of token t; choices of no expert come behind the last
+// expert's rows, so the places are a permutation.
+//
+// Rows: dispatch copies a token's row to the places of its choices (times their
+// weights), combine adds a token's rows up (times the weights, and to a
+// residual).  Each is the other's gradient; the weights' is the dot product of
+// the two rows, which dispatch takes on the way.
+#include "experts.hpp"
+#include "linear_common.hpp"
+#include "mr_common.hpp"
+
+namespace mr {
+
+namespace {
+
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | CTRL, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t min16(uint32_t v) {
+  v = umin(v, ror<8>(v));
+  v = umin(v, ror<4>(v));
+  v = umin(v, ror<2>(v));
+  return umin(v, ror<1>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+  v += __uint_as_float(ror<8>(__float_as_uint(v)));
+  v += __uint_as_float(ror<4>(__float_as_uint(v)));
+  v += __uint_as_float(ror<2>(__float_as_uint(v)));
+  return v + __uint_as_float(ror<1>(__float_as_uint(v)));
+}
+// Over the LPT = 16 or 64 lanes of a token, in each of them.
+template <int LPT>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  return LPT == 16 ? max16(v) : max64(v);
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t min_of(uint32_t v) {
+  v = min16(v);
+  if (LPT == 64) {
+    v = umin(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = umin(v, (uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float sum_of(float v) {
+  v = sum16(v);
+  if (LPT == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+
+// Unsigned numbers in the order of the values: -inf is 0 (never chosen), the
+// zeros are one value, NaN is the largest.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  const uint32_t k = (u >> 31) ? ~u : u | 0x80000000u;
+  return v != v ? 0xffffffffu : u == 0xff800000u ? 0u : k;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+}
+
+// Four consecutive logits from column c, -inf behind the end.
+template <typename T>
+__device__ __forceinline__ void load4(const T* row, int c, int n, float (&v)[4]) {
+  if (c + 4 <= n) {
+    T t[4];
+    if constexpr (sizeof(T) == 4) {
+      const v4u u = *reinterpret_cast<const v4u_any*>(row + c);
+      __builtin_memcpy(t, &u, 16);
+    } else {
+      const v2u u = *reinterpret_cast<const v2u_any*>(row + c);
+      __builtin_memcpy(t, &u, 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = widen(t[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = c + i < n ? widen(row[c + i]) : -__builtin_inff();
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]) {
+  T t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = narrow<T>(v[i]);
+  if (c + 4 <= n) {
+    if constexpr (sizeof(T) == 4) {
+      v4u u;
+      __builtin_memcpy(&u, t, 16);
+      *reinterpret_cast<v4u_any*>(row + c) = u;
+    } else {
+      v2u u;
+      __builtin_memcpy(&u, t, 8);
+      *reinterpret_cast<v2u_any*>(row + c) = u;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (c + i < n) row[c + i] = t[i];
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- routing
+// LPT lanes for each token, Q times four logits in each: columns 4 (lane + LPT q)
+// and the three behind.
+template <typename T, int LPT, int Q>
+__global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
+  constexpr int TPB = 256 / LPT;
+  const int lane = threadIdx.x % LPT;
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.tokens; t0 += (int64_t)gridDim.x * TPB) {
+    // lanes behind the last token work on that one and store nothing
+    const bool held = t0 + threadIdx.x / LPT < a.tokens;
+    const int64_t t = held ? t0 + threadIdx.x / LPT : a.tokens - 1;
+    const T* row = reinterpret_cast<const T*>(a.logits) + t * a.ldl;
+    uint32_t key[4 * Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float v[4];
+      load4<T>(row, 4 * (lane + LPT * q), a.n, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) key[4 * q + i] = key_of(v[i]);
+    }
+    float top = 0.f, all = 0.f, mine = 0.f;
+    int32_t expert = -1;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < 4 * Q; ++i) m = umax(m, key[i]);
+      m = max_of<LPT>(m);
+      if (j == 0) {
+        top = value_of(m);
+        if (!a.normalize) {
+#pragma unroll
+          for (int i = 0; i < 4 * Q; ++i) all += key[i] ? expf(value_of(key[i]) - top) : 0.f;
+        }
+      }
+      // the first of the equal ones
+      uint32_t at = 0xffffffffu;
+#pragma unroll
+      for (int i = 4 * Q - 1; i >= 0; --i) at = key[i] == m ? 4u * LPT * (i / 4) + i % 4 : at;
+      at = at == 0xffffffffu ? at : at + 4u * lane;
+      at = min_of<LPT>(at);
+      const uint32_t here = at - 4u * lane;
+#pragma unroll
+      for (int i = 0; i < 4 * Q; ++i) key[i] = here == 4u * LPT * (i / 4) + i % 4 ? 0u : key[i];
+      if (lane == j && m) {
+        expert = (int32_t)at;
+        mine = expf(value_of(m) - top);
+      }
+    }
+    const float sum = sum_of<LPT>(a.normalize ? mine : all);
+    if (!held) continue;
+    if (lane < a.k) {
+      a.experts[t * a.k + lane] = expert;
+      a.weights[t * a.k + lane] = expert < 0 ? 0.f : mine / sum;
+    }
+    if (lane == 0) a.log_sum[t] = expert < 0 ? -__builtin_inff() : top + logf(sum);
+  }
+}
+
+// One wave for each token, its choices in the first lanes.  The softmax over all
+// experts is worked out again from the logits (ONE: a row's are at most 256, four in
+// each lane): exp(l - log_sum) from a kept log_sum is off by its rounding, which
+// for large logits, or rows at the type's lowest value, is more than the result.
+template <typename T, bool ONE>
+__global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+    int expert = -1;
+    float w = 0.f, dw = 0.f;
+    if (lane < a.k) {
+      expert = a.experts[t * a.k + lane];
+      if (expert >= 0 && expert < a.n) {
+        w = a.weights[t * a.k + lane];
+        dw = a.dweights[t * a.k + lane];
+      } else {
+        expert = -1;
+      }
+    }
+    const T* row = reinterpret_cast<const T*>(a.logits) + t * a.ldl;
+    T* out = reinterpret_cast<T*>(a.dlogits) + t * a.ldd;
+    float v[4], top = -__builtin_inff(), sum = 0.f;
+    if (!a.normalize) {
+      for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {
+        load4<T>(row, c0 + 4 * lane, a.n, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i]);
+      }
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+      for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {
+        if (!ONE) load4<T>(row, c0 + 4 * lane, a.n, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = v[i] == -__builtin_inff() ? 0.f : expf(v[i] - top);
+          sum += v[i];
+        }
+      }
+      sum = sum64(sum);
+    }
+    const float c = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(sum16(w * dw))));
+    const float part = a.normalize ? w * (dw - c) : w * dw;
+    const float share = sum == 0.f ? 0.f : c / sum;
+    for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {
+      const int col = c0 + 4 * lane;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      if (!a.normalize) {
+        if (!ONE) {
+          load4<T>(row, col, a.n, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = v[i] == -__builtin_inff() ? 0.f : expf(v[i] - top);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = -v[i] * share;
+      }
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __builtin_amdgcn_readlane(expert, j) - c0;
+        if (e < 0 || e >= 256) continue;
+        const float p = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(part), j));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] += e == 4 * lane + i ? p : 0.f;
+      }
+      if (col < a.n) store4<T>(out, col, a.n, d);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ order
+namespace {
+
+// Expert of choice f, n where it is none.
+__device__ __forceinline__ int choice(const OrderArgs& a, int f) {
+  const int64_t at = a.lde == a.k ? f : (int64_t)(f / a.k) * a.lde + f % a.k;
+  if (a.wide) {
+    const int64_t e = reinterpret_cast<const int64_t*>(a.experts)[at];
+    return e >= 0 && e < a.n ? (int)e : a.n;
+  }
+  const int e = reinterpret_cast<const int32_t*>(a.experts)[at];
+  return e >= 0 && e < a.n ? e : a.n;
+}
+
+// Exclusive sums of v[0 .. n) in LDS, by the whole workgroup; `waves` has a place for each wave.
+__device__ __forceinline__ void exclusive_sums(int32_t* v, int n, int32_t* waves) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x, first = (int)threadIdx.x * per;
+  int own = 0;
+  for (int i = first; i < first + per && i < n; ++i) own += v[i];
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  __syncthreads();
+  if (lane == 63) waves[wave] = upto;
+  __syncthreads();
+  int before = upto - own;
+  for (int w = 0; w < wave; ++w) before += waves[w];
+  for (int i = first; i < first + per && i < n; ++i) {
+    const int c = v[i];
+    v[i] = before;
+    before += c;
+  }
+  __syncthreads();
+}
+
+}  // namespace
+
+// The places of a workgroup's choices.  Each wave walks its part of them 64 at a
+// time: lanes of one expert find each other by the bits of its number, the
+// first of them keeps the wave's count.  With one workgroup the places are
+// final; else they count from the expert's first row of this workgroup, and
+// order_place_kernel adds where that is.
+__global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
+  extern __shared__ int32_t lds[];  // waves x bins counts, bins totals, 16 for the scan
+  const int bins = a.n + 1, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t* count = lds + wave * bins;
+  int32_t* total = lds + waves * bins;
+  for (int i = threadIdx.x; i < waves * bins; i += blockDim.x) lds[i] = 0;
+  __syncthreads();
+  const int64_t begin = (int64_t)blockIdx.x * a.chunk;
+  const int part = (a.chunk / waves + 63) / 64 * 64;
+  const int64_t from = begin + (int64_t)wave * part;
+  int64_t to = from + part;
+  if (to > begin + a.chunk) to = begin + a.chunk;
+  if (to > a.total) to = a.total;
+  for (int64_t f = from + lane; f - lane < to; f += 64) {
+    const bool valid = f < to;
+    const int e = valid ? choice(a, (int)f) : a.n;
+    uint64_t same = __ballot(valid);
+    for (int b = 0; (bins - 1) >> b; ++b) {
+      const bool bit = (e >> b) & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (valid) {
+      const int prior = count[e];
+      a.place[f] = prior + rank;
+      if (rank == 0) count[e] = prior + __popcll(same);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __syncthreads();
+  // counts to the sums over earlier waves, and the workgroup's totals
+  for (int e = threadIdx.x; e < bins; e += blockDim.x) {
+    int s = 0;
+    for (int w = 0; w < waves; ++w) {
+      const int c = lds[w * bins + e];
+      lds[w * bins + e] = s;
+      s += c;
+    }
+    total[e] = s;
+    if (a.counts) a.counts[(int64_t)blockIdx.x * bins + e] = s;
+  }
+  __syncthreads();
+  if (!a.counts) {
+    exclusive_sums(total, bins, total + bins);
+    for (int e = threadIdx.x; e < bins; e += blockDim.x) a.offsets[e] = total[e];
+  }
+  for (int64_t f = from + lane; f < to; f += 64) {
+    const int e = choice(a, (int)f);
+    a.place[f] += count[e] + (a.counts ? 0 : total[e]);
+  }
+}
+
+// Adds to a workgroup's places the rows of lower experts and of its expert in
+// earlier workgroups.
+__global__ __launch_bounds__(1024) void order_place_kernel(const OrderArgs a) {
+  extern __shared__ int32_t lds[];  // bins totals, bins of earlier workgroups, 16 for the scan
+  const int bins = a.n + 1;
+  int32_t* total = lds;
+  int32_t* before = lds + bins;
+  for (int i = threadIdx.x; i < 2 * bins; i += blockDim.x) lds[i] = 0;
+  __syncthreads();
+  // every bin by as many threads as there are for it
+  const int by = bins < (int)blockDim.x ? (int)blockDim.x / bins : 1;
+  for (int i = threadIdx.x; i < bins * by; i += blockDim.x) {
+    const int e = i % bins;
+    int s = 0, early = 0;
+#pragma unroll 4
+    for (int g = i / bins; g < a.blocks; g += by) {
+      const int c = a.counts[(int64_t)g * bins + e];
+      s += c;
+      early += g < (int)blockIdx.x ? c : 0;
+    }
+    atomicAdd(&total[e], s);
+    atomicAdd(&before[e], early);
+  }
+  __syncthreads();
+  exclusive_sums(total, bins, before + bins);
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < bins; e += blockDim.x) a.offsets[e] = total[e];
+  const int64_t begin = (int64_t)blockIdx.x * a.chunk;
+  const int64_t end = begin + a.chunk < a.total ? begin + a.chunk : a.total;
+  for (int64_t f = begin + threadIdx.x; f < end; f += blockDim.x) {
+    const int e = choice(a, (int)f);
+    a.place[f] += total[e] + before[e];
+  }
+}
+
+// ------------------------------------------------------------------- rows
+namespace {
+
+// How many sorted rows belong to an expert, 0 .. rows.
+__device__ __forceinline__ int64_t held_rows(const RowsArgs& a, int64_t rows) {
+  const int64_t h = a.offsets[a.experts];
+  return h < 0 ? 0 : h < rows ? h : rows;
+}
+template <typename T>
+__device__ __forceinline__ void load_part(const T* row, int c, int width, float (&v)[8]) {
+  if (c + 8 <= width) {
+    widen8(load8<T>(row + c), v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) v[i] = widen(row[c + i]);
+}
+template <typename T>
+__device__ __forceinline__ void store_part(T* row, int c, int width, const float (&v)[8]) {
+  if (c + 8 <= width) {
+    store8<T>(row + c, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) row[c + i] = narrow<T>(v[i]);
+}
+
+constexpr int kPart = 512;  // columns that a wave holds 8 of in each lane
+
+}  // namespace
+
+// A wave for each token and 4 parts of its row: to the places of its choices.
+template <typename T>
+__global__ __launch_bounds__(256) void dispatch_kernel(const RowsArgs a) {
+  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
+  const int c0 = blockIdx.y * CH * kPart + 8 * lane;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ldx;
+    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
+    float v[CH][8];
+#pragma unroll
+    for (int q = 0; q < CH; ++q) load_part<T>(x, c0 + q * kPart, a.width, v[q]);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t p = __builtin_amdgcn_readlane(mine, j);
+      if (p < 0 || p >= rows) continue;
+      T* y = reinterpret_cast<T*>(a.out) + p * a.ldo;
+      if (p < held) {
+#pragma unroll
+        for (int q = 0; q < CH; ++q) store_part<T>(y, c0 + q * kPart, a.width, v[q]);
+      } else {
+        const float zero[8] = {};
+#pragma unroll
+        for (int q = 0; q < CH; ++q) store_part<T>(y, c0 + q * kPart, a.width, zero);
+      }
+    }
+  }
+}
+
+// A wave for each token: its row times the weights to the places of its choices,
+// and its dot products with the rows that lie there.
+template <typename T>
+__global__ __launch_bounds__(256) void dispatch_dot_kernel(const RowsArgs a) {
+  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ldx;
+    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
+    const float weight = lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
+    float dot = 0.f;
+    for (int c0 = 8 * lane; c0 - 8 * lane < a.width; c0 += CH * kPart) {
+      float v[CH][8];
+#pragma unroll
+      for (int q = 0; q < CH; ++q) load_part<T>(x, c0 + q * kPart, a.width, v[q]);
+      for (int j = 0; j < a.k; ++j) {
+        const int64_t p = __builtin_amdgcn_readlane(mine, j);
+        if (p < 0 || p >= rows) continue;
+        T* y = reinterpret_cast<T*>(a.out) + p * a.ldo;
+        const bool in = p < held;
+        const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
+        float s = 0.f;
+        if (in) {
+          const T* z = reinterpret_cast<const T*>(a.rows) + p * a.ldr;
+          float u[CH][8];
+#pragma unroll
+          for (int q = 0; q < CH; ++q) load_part<T>(z, c0 + q * kPart, a.width, u[q]);
+#pragma unroll
+          for (int q = 0; q < CH; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(u[q][i], v[q][i], s);
+        }
+        s = sum64(s);
+        dot += lane == j ? s : 0.f;
+#pragma unroll
+        for (int q = 0; q < CH; ++q) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = in ? w * v[q][i] : 0.f;
+          store_part<T>(y, c0 + q * kPart, a.width, o);
+        }
+      }
+    }
+    if (lane < a.k) a.dots[t * a.k + lane] = dot;
+  }
+}
+
+// A wave for each token and part of its row: its choices that an expert has, in
+// their order, four rows' loads in flight at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void combine_kernel(const RowsArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
+  const int c = blockIdx.y * kPart + 8 * lane;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
+    const float weight = lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
+    uint64_t left = __ballot(mine >= 0 && mine < held);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+    if (a.x && c < a.width) load_part<T>(reinterpret_cast<const T*>(a.x) + t * a.ldx, c, a.width, s);
+    const T* from = reinterpret_cast<const T*>(a.rows) + c;
+    if (c + 8 <= a.width) {
+      auto next = [&](float& w) {
+        const int j = __builtin_ctzll(left);
+        left &= left - 1;
+        w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
+        return load8<T>(from + __builtin_amdgcn_readlane(mine, j) * a.ldr);
+      };
+      auto add = [&](const Raw8<T>& r, float w) {
+        float u[8];
+        widen8(r, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(w, u[i], s[i]);
+      };
+      while (__popcll(left) >= 4) {
+        Raw8<T> r[4];
+        float w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) r[q] = next(w[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) add(r[q], w[q]);
+      }
+      while (left) {
+        float w;
+        const Raw8<T> r = next(w);
+        add(r, w);
+      }
+    } else if (c < a.width) {
+      for (; left; left &= left - 1) {
+        const int j = __builtin_ctzll(left);
+        const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
+        float u[8];
+        load_part<T>(from + __builtin_amdgcn_readlane(mine, j) * a.ldr - c, c, a.width, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(w, u[i], s[i]);
+      }
+    }
+    if (c < a.width) store_part<T>(reinterpret_cast<T*>(a.out) + t * a.ldo, c, a.width, s);
+  }
+}
+
+// ------------------------------------------------------------ launchers
+namespace {
+
+constexpr int64_t kMaxGroups = 1 << 16;  // workgroups along a launch's tokens; each takes every so manieth
+
+template <typename T, int LPT, int Q>
+hipError_t route_go(const RouteArgs& a, hipStream_t s) {
+  constexpr int TPB = 256 / LPT;
+  const int64_t g = (a.tokens + TPB - 1) / TPB;
+  hipLaunchKernelGGL((route_kernel<T, LPT, Q>), dim3((unsigned)(g < kMaxGroups ? g : kMaxGroups)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t route_pick(const RouteArgs& a, hipStream_t s) {
+  if (a.n <= 64) return route_go<T, 16, 1>(a, s);
+  if (a.n <= 128) return route_go<T, 16, 2>(a, s);
+  if (a.n <= 256) return route_go<T, 16, 4>(a, s);
+  if (a.n <= 384) return route_go<T, 16, 6>(a, s);
+  if (a.n <= 512) return route_go<T, 16, 8>(a, s);
+  if (a.n <= 1024) return route_go<T, 64, 4>(a, s);
+  if (a.n <= 2048) return route_go<T, 64, 8>(a, s);
+  return route_go<T, 64, 16>(a, s);
+}
+
+unsigned token_groups(int64_t tokens) {
+  const int64_t g = (tokens + 3) / 4;
+  return (unsigned)(g < kMaxGroups ? g : kMaxGroups);
+}
+
+template <typename T>
+hipError_t dispatch_go(const RowsArgs& a, hipStream_t s) {
+  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
+  if (a.dots) {
+    hipLaunchKernelGGL((dispatch_dot_kernel<T>), dim3(token_groups(a.tokens)), dim3(256), 0, s, a);
+  } else {
+    const unsigned parts = (unsigned)((a.width + CH * kPart - 1) / (CH * kPart));
+    hipLaunchKernelGGL((dispatch_kernel<T>), dim3(token_groups(a.tokens), parts), dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t combine_go(const RowsArgs& a, hipStream_t s) {
+  const unsigned parts = (unsigned)((a.width + kPart - 1) / kPart);
+  hipLaunchKernelGGL((combine_kernel<T>), dim3(token_groups(a.tokens), parts), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, mr_dtype dt, hipStream_t s) {
+  if (dt == MR_F32) return route_pick<float>(a, s);
+  if (dt == MR_F16) return route_pick<_Float16>(a, s);
+  return route_pick<bf16_t>(a, s);
+}
+
+namespace {
+
+template <typename T>
+hipError_t route_grad_go(const RouteGradArgs& a, hipStream_t s) {
+  if (a.n <= 256)
+    hipLaunchKernelGGL((route_grad_kernel<T, true>), dim3(token_groups(a.tokens)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((route_grad_kernel<T, false>), dim3(token_groups(a.tokens)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_grad(const RouteGradArgs& a, mr_dtype dt, hipStream_t s) {
+  if (dt == MR_F32) return route_grad_go<float>(a, s);
+  if (dt == MR_F16) return route_grad_go<_Float16>(a, s);
+  return route_grad_go<bf16_t>(a, s);
+}
+
+void order_plan(int64_t total, int64_t n, int32_t* chunk, int32_t* blocks, int32_t* waves) {
+  // counts of every wave in 64 KB of LDS
+  *waves = n < 900 ? 16 : n < 1800 ? 8 : n < 3000 ? 4 : 2;
+  const int64_t round = 64 * *waves;  // choices that a workgroup looks at at a time
+  int64_t c = (total + round - 1) / round * round;
+  if (total > 16384) {
+    c = 4096;
+    while ((total + c - 1) / c > 256) c *= 2;  // every workgroup reads all workgroups' counts
+  }
+  if (c < round) c = round;
+  *chunk = (int32_t)c;
+  *blocks = total > 16384 ? (int32_t)((total + c - 1) / c) : 1;
+}
+
+hipError_t launch_order(const OrderArgs& a, hipStream_t s) {
+  const size_t bins = (size_t)a.n + 1;
+  hipLaunchKernelGGL(order_rank_kernel, dim3(a.blocks), dim3(64 * a.waves), (bins * (a.waves + 1) + 16) * 4, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.counts) return e;
+  hipLaunchKernelGGL(order_place_kernel, dim3(a.blocks), dim3(1024), (bins * 2 + 16) * 4, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const RowsArgs& a, mr_dtype dt, hipStream_t s) {
+  if (dt == MR_F32) return dispatch_go<float>(a, s);
+  if (dt == MR_F16) return dispatch_go<_Float16>(a, s);
+  return dispatch_go<bf16_t>(a, s);
+}
+
+hipError_t launch_combine(const RowsArgs& a, mr_dtype dt, hipStream_t s) {
+  if (dt == MR_F32) return combine_go<float>(a, s);
+  if (dt == MR_F16) return combine_go<_Float16>(a, s);
+  return combine_go<bf16_t>(a, s);
+}
+
+}  // namespace mr

@@ -37,6 +37,15 @@ class RmsNormOut(NamedTuple):
     scales: Optional[torch.Tensor]
 
 
+class LayerNormOut(NamedTuple):
+    h: torch.Tensor  # x + residual (x itself without a residual)
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    y: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
 class Quantized(NamedTuple):
     q: Optional[torch.Tensor]
     scales: Optional[torch.Tensor]
@@ -176,6 +185,76 @@ def rms_norm_backward(dy, h, rstd, weight, dresidual=None, weight_grad: bool = T
         _in_use_on(stream, ws, dx, dweight)
     _check(lib.rms_norm_backward(addressof(p), _ptr(ws), need, _stream(stream, dev)))
     return dx, dweight
+
+
+def layer_norm_forward(x, weight, bias, eps: float, residual=None, keep_y: bool = True, eight: Optional[str] = None,
+                       stream=None) -> LayerNormOut:
+    """Layer norm of the rows of x (+ residual), y = (h - mean) rstd weight + bias.
+
+    x, residual: (rows, width) of one type, float32, float16 or bfloat16;
+    weight, bias: (width,), both float32 or both of that type; bias may be None.
+    keep_y and eight as in rms_norm_forward.
+    """
+    dev = _device(x, weight, bias, residual)
+    code = _float_code(x, "x")
+    rows, width = x.shape
+    w_code = _norm_weight(weight, x)
+    if bias is not None and _norm_weight(bias, x) != w_code:
+        raise ValueError("bias must have weight's type")
+    if residual is not None:
+        _same_shape("residual", residual, x.shape)
+        if residual.dtype != x.dtype:
+            raise ValueError("residual must have x's type")
+    if not keep_y and eight is None:
+        raise ValueError("keep_y or eight: one output at least")
+    with _memory_of(stream):
+        h = torch.empty(rows, width, dtype=x.dtype, device=dev) if residual is not None else None
+        mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=dev).unbind(0)
+        y = torch.empty(rows, width, dtype=x.dtype, device=dev) if keep_y else None
+        q = _eight(rows, width, eight, dev) if eight is not None else None
+        scales = torch.empty(rows, _blocks(width), dtype=torch.float32, device=dev) if eight is not None else None
+    p = B.LayerNormProblem(rows, width, _ptr(x), _ld(x), _ptr(residual), _ld(residual) if residual is not None else 0,
+                           _ptr(weight), _ptr(bias), _ptr(h), width, _ptr(mean), _ptr(rstd), _ptr(y), width, _ptr(q),
+                           (width + 15) // 16 * 16, _ptr(scales), _blocks(width), code, w_code,
+                           _EIGHTS[q.dtype] if q is not None else 0, 0, float(eps))
+    if stream is not None:
+        _in_use_here(stream, h, mean, rstd, y, q, scales)
+        _in_use_on(stream, h, mean, rstd, y, q, scales)
+    _check(library().layer_norm_forward(addressof(p), _stream(stream, dev)))
+    return LayerNormOut(h if residual is not None else x, mean, rstd, y, q, scales)
+
+
+def layer_norm_backward(dy, h, mean, rstd, weight, dresidual=None, weight_grad: bool = True, stream=None):
+    """(dx, dweight, dbias) of layer_norm_forward: dx of dy's type is the gradient
+    of x and of the residual, with dresidual (what reaches h by the residual path)
+    added; dweight and dbias (width,) float32, or None without weight_grad."""
+    dev = _device(dy, h, mean, rstd, weight, dresidual)
+    code = _float_code(dy, "dy")
+    rows, width = dy.shape
+    for name, t in (("h", h), ("dresidual", dresidual)):
+        if t is not None:
+            _same_shape(name, t, dy.shape)
+            if t.dtype != dy.dtype:
+                raise ValueError(f"{name} must have dy's type")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != rows or (rows > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be contiguous float32, one value per row")
+    w_code = _norm_weight(weight, dy)
+    with _memory_of(stream):
+        dx = torch.empty(rows, width, dtype=dy.dtype, device=dev)
+        dweight, dbias = torch.empty(2, width, dtype=torch.float32, device=dev).unbind(0) if weight_grad else (None, None)
+    p = B.LayerNormGradProblem(rows, width, _ptr(dy), _ld(dy), _ptr(h), _ld(h), _ptr(mean), _ptr(rstd), _ptr(weight),
+                               _ptr(dresidual), _ld(dresidual) if dresidual is not None else 0, _ptr(dx), width,
+                               _ptr(dweight), _ptr(dbias), code, w_code)
+    lib = library()
+    need = lib.layer_norm_backward_workspace(addressof(p))
+    with _memory_of(stream):
+        ws = _workspace(need, dev)
+    if stream is not None:
+        _in_use_here(stream, dx, dweight, dbias)
+        _in_use_on(stream, ws, dx, dweight, dbias)
+    _check(lib.layer_norm_backward(addressof(p), _ptr(ws), need, _stream(stream, dev)))
+    return dx, dweight, dbias
 
 
 def quantize_blocks(x, eight: str = "e4m3", block: str = "vector", order: str = "rows", stream=None) -> Quantized:
