@@ -217,7 +217,12 @@ namespace {
 constexpr int64_t kMaxValues = int64_t(1) << 40;  // of a gradient
 constexpr int64_t kClipUnits = 2048;              // of 8 values: a workgroup's least share
 
-int64_t clip_units(const mr_clip_problem& p) { return p.m * ((p.n + 7) / 8); }
+bool clip_flat(const mr_clip_problem& p) { return p.m <= 1 || (p.ldg == p.n && (!p.OUT || p.ldo == p.n)); }
+
+// Units of eight values, or what is left of a row.
+int64_t clip_units(const mr_clip_problem& p) {
+  return clip_flat(p) ? (p.m * p.n + 7) / 8 : p.m * ((p.n + 7) / 8);
+}
 
 // Units of 8 values for each workgroup of a call: all workgroups are resident at
 // once (8 on each of 256 CUs, and one more for each gradient), and a few
@@ -225,7 +230,7 @@ int64_t clip_units(const mr_clip_problem& p) { return p.m * ((p.n + 7) / 8); }
 int64_t clip_per_block(const mr_clip_problem* p, int32_t count) {
   int64_t all = 0;
   for (int i = 0; i < count; ++i) all += clip_units(p[i]);
-  const int64_t per = (all / 2048 + 255) / 256 * 256;
+  const int64_t per = (all / 2048 + 1023) / 1024 * 1024;
   return per < kClipUnits ? kClipUnits : per;
 }
 int64_t clip_blocks(const mr_clip_problem& p, int64_t per) {
@@ -236,8 +241,42 @@ bool clip_shape(const mr_clip_problem& p) {
   return p.m >= 0 && p.n >= 0 && p.m <= kMaxValues && p.n <= kMaxValues && (p.n == 0 || p.m <= kMaxValues / p.n);
 }
 
-// Workspace: partial sums, the factor, each gradient's first sum.
-size_t clip_first_at(int64_t slots) { return align256((size_t)(slots + 1) * sizeof(double)); }
+// More partial sums than this are added up by a launch of their own, fewer by every workgroup of the scaling.
+constexpr int64_t kClipSums = 4096;
+
+// The call's launches of one kind of gradients, from its `slot`th workgroup on.
+template <typename Jobs, typename Launch>
+mr_status clip_batches(const mr_clip_problem* p, int32_t count, ClipBatch<Jobs>& b, int64_t& slot, Launch&& launch) {
+  b.njobs = b.blocks = 0;
+  b.slot = (int32_t)slot;
+  auto flush = [&]() -> mr_status {
+    if (b.njobs == 0) return MR_OK;
+    MR_TRY(launch(b));
+    slot += b.blocks;
+    b.njobs = b.blocks = 0;
+    b.slot = (int32_t)slot;
+    return MR_OK;
+  };
+  for (int i = 0; i < count; ++i) {
+    const mr_clip_problem& q = p[i];
+    if (clip_flat(q) == Jobs::kRows) continue;
+    const int j = b.njobs++;
+    b.job.g[j] = q.G;
+    b.job.out[j] = q.OUT ? q.OUT : q.G;
+    b.job.type[j] = (uint8_t)(q.dtype | (q.OUT ? q.out_dtype : q.dtype) << 4);
+    b.job.problem[j] = i;
+    b.job.begin[j] = b.blocks;
+    if constexpr (Jobs::kRows) {
+      b.job.cols[j] = q.n, b.job.rows[j] = q.m;
+      b.job.ldg[j] = q.ldg, b.job.ldo[j] = q.OUT ? q.ldo : q.ldg;
+    } else {
+      b.job.cols[j] = q.m * q.n;
+    }
+    b.blocks += (int32_t)clip_blocks(q, b.per);
+    if (b.njobs == Jobs::kJobs) MR_TRY(flush());
+  }
+  return flush();
+}
 
 }  // namespace
 
@@ -250,7 +289,7 @@ size_t clip_gradients_batched_workspace(const mr_clip_problem* p, int32_t count)
   const int64_t per = clip_per_block(p, count);
   int64_t slots = 0;
   for (int i = 0; i < count; ++i) slots += clip_blocks(p[i], per);
-  return clip_first_at(slots) + align256((size_t)count * sizeof(int32_t));
+  return align256((size_t)(slots + 1) * sizeof(double));
 }
 
 mr_status clip_gradients_batched(const mr_clip_problem* p, int32_t count, double max_norm, double* norms_dev, void* ws,
@@ -295,40 +334,30 @@ mr_status clip_gradients_batched(const mr_clip_problem* p, int32_t count, double
   for (int i = 0; i < count; ++i) slots += clip_blocks(p[i], per);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   double* partial = static_cast<double*>(ws);
-  double* by = count > 0 ? partial + slots : nullptr;
-  int32_t* first = count > 0 ? reinterpret_cast<int32_t*>(static_cast<char*>(ws) + clip_first_at(slots)) : nullptr;
-  auto over_jobs = [&](auto&& launch) -> mr_status {
+  const bool fold = slots > kClipSums;
+  auto over = [&](auto&& launch) -> mr_status {
     int64_t slot = 0;
-    for (int i0 = 0; i0 < count; i0 += kMaxClipJobs) {
-      ClipBatch b;
-      memset(&b, 0, sizeof b);
-      b.partial = partial, b.first = first, b.by = by, b.per_block = per, b.first_problem = i0;
-      for (int i = i0; i < count && b.njobs < kMaxClipJobs; ++i) {
-        const mr_clip_problem& q = p[i];
-        ClipJob& J = b.job[b.njobs++];
-        const bool flat = q.m <= 1 || (q.ldg == q.n && (!q.OUT || q.ldo == q.n));
-        J.g = q.G, J.out = q.OUT ? q.OUT : q.G;
-        J.rows = flat ? 1 : q.m, J.cols = flat ? q.m * q.n : q.n;
-        J.ldg = q.ldg, J.ldo = q.OUT ? q.ldo : q.ldg;
-        J.block_begin = b.total_blocks, J.slot = (int32_t)slot;
-        J.dtype = q.dtype, J.out_dtype = q.OUT ? q.out_dtype : q.dtype;
-        const int64_t blocks = clip_blocks(q, per);
-        b.total_blocks += (int32_t)blocks;
-        slot += blocks;
-      }
-      MR_TRY(launch(b));
-    }
-    return MR_OK;
+    ClipBatch<ClipFlat> f;
+    ClipBatch<ClipRows> r;
+    memset(&f, 0, sizeof f);
+    memset(&r, 0, sizeof r);
+    f.partial = r.partial = partial;
+    f.sums = r.sums = fold ? partial + slots : partial;
+    f.nsums = r.nsums = fold ? 1 : (int32_t)slots;
+    f.norms = r.norms = norms_dev;
+    f.max_norm = r.max_norm = max_norm;
+    f.per = r.per = per;
+    MR_TRY(clip_batches(p, count, f, slot, launch));
+    return clip_batches(p, count, r, slot, launch);
   };
-  if (count > 0)
-    MR_TRY(over_jobs([&](const ClipBatch& b) {
-      return traced(kTrClipNorm, true, s, [&] { return launch_clip_squares(b, s); }, "clip squares launch");
-    }));
-  MR_TRY(traced(kTrClipNorm, true, s,
-                [&] { return launch_clip_norms(partial, first, count, (int)slots, max_norm, norms_dev, by, s); },
-                "clip norms launch"));
-  if (count == 0) return MR_OK;
-  return over_jobs([&](const ClipBatch& b) {
+  MR_TRY(over([&](const auto& b) {
+    return traced(kTrClipNorm, true, s, [&] { return launch_clip_squares(b, s); }, "clip squares launch");
+  }));
+  if (fold || count == 0)
+    MR_TRY(traced(kTrClipNorm, true, s,
+                  [&] { return launch_clip_fold(partial, (int)slots, count ? partial + slots : norms_dev, s); },
+                  "clip fold launch"));
+  return over([&](const auto& b) {
     return traced(kTrClipScale, true, s, [&] { return launch_clip_scale(b, s); }, "clip scale launch");
   });
 }
