@@ -106,6 +106,19 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
   }
 }
 
+// A row's eight values of a chunk as they are stored, 0 behind its end.
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_chunk(const T* row, int c, int width) {
+  if (c + 8 <= width) return load8<T>(row + c);
+  T t[8] = {};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (c + i < width) t[i] = row[c + i];
+  Raw8<T> r;
+  __builtin_memcpy(&r, t, sizeof r);
+  return r;
+}
+
 // Rows r0, r0 + gridDim RPB, ...: dx, and this workgroup's column sums of dy hh
 // and of dy into a.partial[2 blockIdx.x] and the row behind it.
 template <typename T, int TPR, int CH>
@@ -120,42 +133,49 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
   for (int k = 0; k < CH; ++k)
 #pragma unroll
     for (int i = 0; i < NV; ++i) dw[k][i] = db[k][i] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t r = RPB == 1 ? r0 : r0 + threadIdx.x / TPR;
-    asm volatile("" : "+v"(t));  // columns and addresses are worked out per row, not kept in registers over the loop
-    if (TPR == 64 && r >= a.rows) break;  // whole waves: the barriers below come after the loop
-    const T* dy = reinterpret_cast<const T*>(a.dy) + r * a.lddy;
-    const T* h = reinterpret_cast<const T*>(a.x) + r * a.ldx;
-    const float rho = a.rstd_in[r], mu = a.mean_in[r];
-    float g[CH][NV], hh[CH][NV];
-    float sg = 0.f, dot = 0.f;
+  Raw8<T> dy[CH], h[CH];
+  float rho = 0.f, mu = 0.f;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  // the next row's loads are under way while one is worked on, but for the widest of float32, which takes all registers
+  constexpr bool kAhead = sizeof(T) == 2 || TPR < 512;
+  auto load = [&](int64_t r) {
+    const T* from_dy = reinterpret_cast<const T*>(a.dy) + r * a.lddy;
+    const T* from_h = reinterpret_cast<const T*>(a.x) + r * a.ldx;
+    rho = a.rstd_in[r], mu = a.mean_in[r];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      load_chunk<T>(dy, chunk_col<TPR>(t, k), a.width, g[k]);
-      load_chunk<T>(h, chunk_col<TPR>(t, k), a.width, hh[k]);
+      dy[k] = raw_chunk<T>(from_dy, chunk_col<TPR>(t, k), a.width);
+      h[k] = raw_chunk<T>(from_h, chunk_col<TPR>(t, k), a.width);
     }
+  };
+  int64_t r = (int64_t)blockIdx.x * RPB + (RPB == 1 ? 0 : threadIdx.x / TPR);
+  if (r < a.rows) load(r);
+  while (r < a.rows) {  // whole waves (RPB > 1) or the whole workgroup: the barriers below come after the loop
+    asm volatile("" : "+v"(t));  // columns and addresses are worked out per row, not kept in registers over the loop
+    float sg = 0.f, dot = 0.f;
+    Raw8<T> now_dy[CH], now_h[CH], rr[CH];
+    const float now_rho = rho, now_mu = mu;
+    const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      float w[NV];
+      now_dy[k] = dy[k], now_h[k] = h[k];
+      if (res) rr[k] = raw_chunk<T>(res, chunk_col<TPR>(t, k), a.width);
+    }
+    if (kAhead && r + step < a.rows) load(r + step);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      float w[NV], g[NV], hh[NV];
       load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
+      widen8(now_dy[k], g);
+      widen8(now_h[k], hh);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        hh[k][i] = (hh[k][i] - mu) * rho;
-        dw[k][i] = fmaf(g[k][i], hh[k][i], dw[k][i]);
-        db[k][i] += g[k][i];
-        g[k][i] *= w[i];  // 0 behind the row's end
-        sg += g[k][i];
-        dot = fmaf(g[k][i], hh[k][i], dot);
-      }
-    }
-    // under way during the reduction
-    const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
-    Raw8<T> rr[CH];
-    if (res) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int col = chunk_col<TPR>(t, k);
-        if (col + 8 <= a.width) rr[k] = load8<T>(res + col);
+        hh[i] = (hh[i] - now_mu) * now_rho;
+        dw[k][i] = fmaf(g[i], hh[i], dw[k][i]);
+        db[k][i] += g[i];
+        g[i] *= w[i];  // 0 behind the row's end
+        sg += g[i];
+        dot = fmaf(g[i], hh[i], dot);
       }
     }
     row_sum2<TPR>(sg, dot, red);
@@ -163,20 +183,19 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
     T* dx = reinterpret_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      float u[NV];
+      float w[NV], g[NV], hh[NV], u[NV];
+      load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
+      widen8(now_dy[k], g);
+      widen8(now_h[k], hh);
 #pragma unroll
       for (int i = 0; i < NV; ++i) u[i] = 0.f;
-      if (res) {
-        const int col = chunk_col<TPR>(t, k);
-        if (col + 8 <= a.width)
-          widen8(rr[k], u);
-        else
-          load_chunk<T>(res, col, a.width, u);
-      }
+      if (res) widen8(rr[k], u);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) u[i] += rho * (g[k][i] - c0 - hh[k][i] * c1);
+      for (int i = 0; i < NV; ++i) u[i] += now_rho * (g[i] * w[i] - c0 - (hh[i] - now_mu) * now_rho * c1);
       store_chunk<T>(dx, chunk_col<TPR>(t, k), a.width, u);
     }
+    if (!kAhead && r + step < a.rows) load(r + step);
+    r += step;
   }
   if (!a.partial) return;
   float* out = a.partial + 2 * (int64_t)blockIdx.x * a.width;
