@@ -794,7 +794,7 @@ mr_status route_tokens_backward(const mr_route_grad_problem* problem, void* hip_
  * Choices of no expert (a number outside 0 .. experts - 1) come last, from
  * offsets[experts] on, so the places are a permutation of 0 .. tokens k - 1.
  * experts in [1, 4096], k in [1, 64], tokens k < 2^31.  Workspace:
- * order_by_expert_workspace bytes (0 for up to 16384 choices), 256-byte aligned.
+ * order_by_expert_workspace bytes (0 for a few thousand choices), 256-byte aligned.
  */
 typedef struct {
   int64_t tokens, experts, k;

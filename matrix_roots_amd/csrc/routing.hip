@@ -246,6 +246,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) 
 // ------------------------------------------------------------------ order
 namespace {
 
+constexpr int kRound = 4;
+
 // Expert of choice f, n where it is none.
 __device__ __forceinline__ int choice(const OrderArgs& a, int f) {
   const int64_t at = a.lde == a.k ? f : (int64_t)(f / a.k) * a.lde + f % a.k;
@@ -284,63 +286,75 @@ __device__ __forceinline__ void exclusive_sums(int32_t* v, int n, int32_t* waves
 
 }  // namespace
 
-// The places of a workgroup's choices.  Each wave walks its part of them 64 at a
-// time: lanes of one expert find each other by the bits of its number, the
-// first of them keeps the wave's count.  With one workgroup the places are
-// final; else they count from the expert's first row of this workgroup, and
-// order_place_kernel adds where that is.
+// The places of a workgroup's choices, in rounds of kRound for each lane.  In a
+// round each wave takes the next 64 kRound: lanes of one expert find each other by
+// the bits of its number, the first of them keeps the wave's count.  With one
+// workgroup, and one round, the places are final; else they count from the
+// expert's first row of this workgroup, and order_place_kernel adds where that is.
 __global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
   extern __shared__ int32_t lds[];  // waves x bins counts, bins totals, 16 for the scan
   const int bins = a.n + 1, waves = blockDim.x >> 6;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int32_t* count = lds + wave * bins;
   int32_t* total = lds + waves * bins;
-  for (int i = threadIdx.x; i < waves * bins; i += blockDim.x) lds[i] = 0;
-  __syncthreads();
   const int64_t begin = (int64_t)blockIdx.x * a.chunk;
-  const int part = (a.chunk / waves + 63) / 64 * 64;
-  const int64_t from = begin + (int64_t)wave * part;
-  int64_t to = from + part;
-  if (to > begin + a.chunk) to = begin + a.chunk;
-  if (to > a.total) to = a.total;
-  for (int64_t f = from + lane; f - lane < to; f += 64) {
-    const bool valid = f < to;
-    const int e = valid ? choice(a, (int)f) : a.n;
-    uint64_t same = __ballot(valid);
-    for (int b = 0; (bins - 1) >> b; ++b) {
-      const bool bit = (e >> b) & 1;
-      const uint64_t set = __ballot(bit);
-      same &= bit ? set : ~set;
+  const int64_t end = begin + a.chunk < a.total ? begin + a.chunk : a.total;
+  const int round = (int)blockDim.x * kRound;
+  int64_t f = end;
+  int e[kRound], rank[kRound];
+  for (int i = threadIdx.x; i < bins; i += blockDim.x) total[i] = 0;
+  for (int64_t f0 = begin; f0 < end; f0 += round) {
+    f = f0 + wave * 64 * kRound + lane;
+#pragma unroll
+    for (int r = 0; r < kRound; ++r) e[r] = f + 64 * r < end ? choice(a, (int)(f + 64 * r)) : a.n;
+    for (int i = threadIdx.x; i < waves * bins; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRound; ++r) {
+      const bool valid = f + 64 * r < end;
+      uint64_t same = __ballot(valid);
+      for (int b = 0; (bins - 1) >> b; ++b) {
+        const bool bit = (e[r] >> b) & 1;
+        const uint64_t set = __ballot(bit);
+        same &= bit ? set : ~set;
+      }
+      const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+      if (valid) {
+        const int prior = count[e[r]];
+        rank[r] = prior + before;
+        if (before == 0) count[e[r]] = prior + __popcll(same);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-    if (valid) {
-      const int prior = count[e];
-      a.place[f] = prior + rank;
-      if (rank == 0) count[e] = prior + __popcll(same);
+    __syncthreads();
+    // the waves' counts to the sums over what comes before them
+    for (int i = threadIdx.x; i < bins; i += blockDim.x) {
+      int s = total[i];
+#pragma unroll 4
+      for (int w = 0; w < waves; ++w) {
+        const int c = lds[w * bins + i];
+        lds[w * bins + i] = s;
+        s += c;
+      }
+      total[i] = s;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __syncthreads();
+    if (!a.counts) break;  // one workgroup has one round
+#pragma unroll
+    for (int r = 0; r < kRound; ++r)
+      if (f + 64 * r < end) a.place[f + 64 * r] = rank[r] + count[e[r]];
+    __syncthreads();
+  }
+  if (a.counts) {
+    for (int i = threadIdx.x; i < bins; i += blockDim.x) a.counts[(int64_t)blockIdx.x * bins + i] = total[i];
+    return;
   }
   __syncthreads();
-  // counts to the sums over earlier waves, and the workgroup's totals
-  for (int e = threadIdx.x; e < bins; e += blockDim.x) {
-    int s = 0;
-    for (int w = 0; w < waves; ++w) {
-      const int c = lds[w * bins + e];
-      lds[w * bins + e] = s;
-      s += c;
-    }
-    total[e] = s;
-    if (a.counts) a.counts[(int64_t)blockIdx.x * bins + e] = s;
-  }
-  __syncthreads();
-  if (!a.counts) {
-    exclusive_sums(total, bins, total + bins);
-    for (int e = threadIdx.x; e < bins; e += blockDim.x) a.offsets[e] = total[e];
-  }
-  for (int64_t f = from + lane; f < to; f += 64) {
-    const int e = choice(a, (int)f);
-    a.place[f] += count[e] + (a.counts ? 0 : total[e]);
-  }
+  exclusive_sums(total, bins, total + bins);
+  for (int i = threadIdx.x; i < bins; i += blockDim.x) a.offsets[i] = total[i];
+#pragma unroll
+  for (int r = 0; r < kRound; ++r)
+    if (f + 64 * r < end) a.place[f + 64 * r] = rank[r] + count[e[r]] + total[e[r]];
 }
 
 // Adds to a workgroup's places the rows of lower experts and of its expert in
@@ -372,9 +386,19 @@ __global__ __launch_bounds__(1024) void order_place_kernel(const OrderArgs a) {
     for (int e = threadIdx.x; e < bins; e += blockDim.x) a.offsets[e] = total[e];
   const int64_t begin = (int64_t)blockIdx.x * a.chunk;
   const int64_t end = begin + a.chunk < a.total ? begin + a.chunk : a.total;
-  for (int64_t f = begin + threadIdx.x; f < end; f += blockDim.x) {
-    const int e = choice(a, (int)f);
-    a.place[f] += total[e] + before[e];
+  for (int64_t f = begin + threadIdx.x; f < end; f += blockDim.x * kRound) {
+    int e[kRound], p[kRound];
+#pragma unroll
+    for (int r = 0; r < kRound; ++r) {
+      const int64_t g = f + (int64_t)blockDim.x * r;
+      e[r] = g < end ? choice(a, (int)g) : 0;
+      p[r] = g < end ? a.place[g] : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < kRound; ++r) {
+      const int64_t g = f + (int64_t)blockDim.x * r;
+      if (g < end) a.place[g] = p[r] + total[e[r]] + before[e[r]];
+    }
   }
 }
 
@@ -496,8 +520,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void combine_kernel(const RowsArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
-  const int c = blockIdx.y * kPart + 8 * lane;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
+  const int parts = (a.width + kPart - 1) / kPart;
+  const int64_t jobs = a.tokens * parts;
+  for (int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < jobs; job += (int64_t)gridDim.x * 4) {
+    const int64_t t = jobs >> 31 ? job / parts : (int)job / parts;
+    const int c = (int)(job - t * parts) * kPart + 8 * lane;
     const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
     const float weight = lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
     uint64_t left = __ballot(mine >= 0 && mine < held);
@@ -588,8 +615,7 @@ hipError_t dispatch_go(const RowsArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t combine_go(const RowsArgs& a, hipStream_t s) {
-  const unsigned parts = (unsigned)((a.width + kPart - 1) / kPart);
-  hipLaunchKernelGGL((combine_kernel<T>), dim3(token_groups(a.tokens), parts), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((combine_kernel<T>), dim3(token_groups(a.tokens * ((a.width + kPart - 1) / kPart))), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -623,15 +649,11 @@ hipError_t launch_route_grad(const RouteGradArgs& a, mr_dtype dt, hipStream_t s)
 void order_plan(int64_t total, int64_t n, int32_t* chunk, int32_t* blocks, int32_t* waves) {
   // counts of every wave in 64 KB of LDS
   *waves = n < 900 ? 16 : n < 1800 ? 8 : n < 3000 ? 4 : 2;
-  const int64_t round = 64 * *waves;  // choices that a workgroup looks at at a time
-  int64_t c = (total + round - 1) / round * round;
-  if (total > 16384) {
-    c = 4096;
-    while ((total + c - 1) / c > 256) c *= 2;  // every workgroup reads all workgroups' counts
-  }
-  if (c < round) c = round;
+  const int64_t round = 64 * kRound * *waves;
+  int64_t c = round;
+  while ((total + c - 1) / c > 256) c *= 2;  // every workgroup reads all workgroups' counts
   *chunk = (int32_t)c;
-  *blocks = total > 16384 ? (int32_t)((total + c - 1) / c) : 1;
+  *blocks = total > c ? (int32_t)((total + c - 1) / c) : 1;
 }
 
 hipError_t launch_order(const OrderArgs& a, hipStream_t s) {

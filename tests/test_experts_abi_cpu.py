@@ -133,8 +133,8 @@ def test_order_refusals(lib, change, status):
 
 
 def test_order_workspace(lib):
-    assert lib.order_by_expert_workspace(at(order(tokens=16384, k=1, ldc=1))) == 0
-    p = order(tokens=16385, k=1, ldc=1)
+    assert lib.order_by_expert_workspace(at(order(tokens=4096, k=1, ldc=1))) == 0
+    p = order(tokens=4097, k=1, ldc=1)
     need = lib.order_by_expert_workspace(at(p))
     assert need > 0 and need % 256 == 0
     assert lib.order_by_expert(at(p), None, 0, None) == WORKSPACE
