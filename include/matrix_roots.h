@@ -749,8 +749,8 @@ mr_status grouped_weight_grad(const mr_grouped_grad_problem* problem, void* hip_
  * the lowest index.  -inf is never chosen; where fewer than k are left, `chosen`
  * is -1 and the weight 0.  With S all experts (normalize 0) or the chosen (1):
  *   log_sum = log sum_{e in S} exp(l_e),  weight_j = exp(l_{chosen_j} - log_sum),
- * log_sum -inf for a token without experts.  NaN counts as the largest; a row
- * that holds one, or +inf, gets experts and NaN weights.  experts in [1, 4096],
+ * log_sum -inf for a token without experts.  NaN counts as +inf; a row that holds
+ * either gets experts and NaN weights.  experts in [1, 4096],
  * k in [1, min(16, experts)].
  */
 typedef struct {

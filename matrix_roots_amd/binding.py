@@ -222,6 +222,9 @@ class ClipProblem(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32)]
 
 
+assert ctypes.sizeof(ClipProblem) == 56
+
+
 ROOT_INFO_DTYPE = np.dtype([("scale", "<f8"), ("bound", "<f8"), ("iters", "<i4"), ("fp64_iters", "<i4"),
                             ("residual", "<f4"), ("flags", "<u4"), ("final_degree", "<i4"), ("reserved", "<i4")])
 ROOT_INFO_BYTES = ROOT_INFO_DTYPE.itemsize
@@ -703,8 +706,6 @@ def _rows_of(t):
     if t.is_contiguous():
         return 1, t.numel(), 0
     dims = sorted(((st, n) for st, n in zip(t.stride(), t.shape) if n != 1), reverse=True)
-    if t.numel() == 0:
-        return 1, 0, 0
     if dims[-1][0] != 1:
         raise ValueError("gradients need a dimension of unit stride")
     m, n, ld = 1, 1, 0
@@ -720,52 +721,68 @@ def _rows_of(t):
     return m, n, ld
 
 
+def _current_gpu() -> int:
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _clip_problem(i, g, o, code, codes, f32):
+    """Fields of a mr_clip_problem for gradient g and output o (None: in place)."""
+    if o is None:
+        m, n, ld = _rows_of(g)
+        return m, n, g.data_ptr(), ld, 0, 0, code | code << 32
+    if o.shape != g.shape or o.get_device() != g.get_device():
+        raise ValueError(f"output {i} does not match its gradient")
+    if o.dtype != g.dtype and o.dtype != f32:
+        raise ValueError(f"output {i} is {o.dtype}: the gradient's type or float32 is needed")
+    if g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride():
+        m, n, ld = _rows_of(g)
+        ldo = ld
+    elif g.dim() == 2 and g.stride(1) == 1 and o.stride(1) == 1:
+        (m, n), ld, ldo = g.shape, g.stride(0), o.stride(0)
+    else:
+        raise ValueError(f"output {i} must lie as its gradient does")
+    return m, n, g.data_ptr(), ld, o.data_ptr(), ldo, code | codes[o.dtype] << 32
+
+
 def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequence] = None,
                            return_norms: bool = False, stream=None):
     """Scales the gradients by max_norm / n where their common norm n is finite and
     larger than max_norm; in place, or into `outs`, which hold the gradients in
     either case then.
 
-    grads: float32, float16 or bfloat16 device tensors of any shape whose values
-    lie in rows one stride apart; outs: tensors of the same shapes and strides'
-    order, of the gradient's type or float32 (as gram_ema_update takes them).
+    grads: float32, float16 or bfloat16 tensors on the current GPU, of any shape,
+    whose values lie in rows one stride apart; outs: tensors of the same shapes
+    that lie alike, of the gradient's type or float32 (as gram_ema_update takes
+    them).  No two may share the bytes between their first and last values.
     Returns n, a float64 device scalar; with return_norms (n, norms), the
     gradients' own norms.  max_norm math.inf: the norms alone.
     """
     import torch
 
-    codes = {torch.float32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
+    f32 = torch.float32
+    codes = {f32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
     lib = library()
     count = len(grads)
     if count == 0:
         raise ValueError("no gradients")
     if outs is not None and len(outs) != count:
         raise ValueError("one output per gradient")
-    dev = grads[0].device
-    probs = (ClipProblem * count)()
+    gpu = _current_gpu()
+    fields = []
     for i, g in enumerate(grads):
         code = codes.get(g.dtype)
         if code is None:
             raise ValueError(f"gradient {i} is {g.dtype}: float32, float16 or bfloat16 is needed")
-        if g.device != dev:
-            raise ValueError("all gradients must be on one device")
-        if outs is None:
-            m, n, ld = _rows_of(g)
-            probs[i] = ClipProblem(m, n, g.data_ptr(), ld, 0, 0, code, code)
-            continue
-        o = outs[i]
-        if o.shape != g.shape or o.device != dev:
-            raise ValueError(f"output {i} does not match its gradient")
-        if o.dtype != g.dtype and o.dtype != torch.float32:
-            raise ValueError(f"output {i} is {o.dtype}: the gradient's type or float32 is needed")
-        if g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride():
-            m, n, ld = _rows_of(g)
-            ldo = ld
-        elif g.dim() == 2 and g.stride(1) == 1 and o.stride(1) == 1:
-            (m, n), ld, ldo = g.shape, g.stride(0), o.stride(0)
+        if g.get_device() != gpu:
+            raise ValueError(f"gradient {i} is not on the current GPU")
+        if outs is None and g.is_contiguous():
+            fields += (1, g.numel(), g.data_ptr(), 0, 0, 0, code | code << 32)
         else:
-            raise ValueError(f"output {i} must lie as its gradient does")
-        probs[i] = ClipProblem(m, n, g.data_ptr(), ld, o.data_ptr(), ldo, code, codes[o.dtype])
+            fields += _clip_problem(i, g, None if outs is None else outs[i], code, codes, f32)
+    probs = (ctypes.c_int64 * len(fields))(*fields)  # of mr_clip_problem: seven of 8 bytes, the types in the last
+    dev = grads[0].device
     need = lib.clip_gradients_batched_workspace(ctypes.addressof(probs), count)
     with _memory_of(stream):
         ws = _workspace(need, dev)

@@ -21,7 +21,7 @@ namespace mr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // units of eight values that a thread loads before it works on them
+constexpr int kAhead = 8;  // loads of a thread before it works on their values
 
 __device__ __forceinline__ double sum64d(double v) {
 #pragma unroll
@@ -47,64 +47,85 @@ __device__ __forceinline__ int job_of(const ClipBatch<Jobs>& B, int b) {
   return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_some(const T* p, int64_t n) {
-  T t[8] = {};
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < n) t[i] = p[i];
-  Raw8<T> r;
-  __builtin_memcpy(&r, t, sizeof r);
-  return r;
+// V values as they are stored, at any address: 8 or 16 bytes in one load.
+template <typename T, int V>
+struct Values {
+  typedef uint32_t u __attribute__((ext_vector_type(sizeof(T) * V / 4)));
+  typedef u any __attribute__((aligned(1)));
+};
+template <int V, typename T>
+__device__ __forceinline__ void load_values(const T* p, T (&v)[V]) {
+  const typename Values<T, V>::u r = *reinterpret_cast<const typename Values<T, V>::any*>(p);
+  __builtin_memcpy(v, &r, sizeof r);
 }
-template <typename T>
-__device__ __forceinline__ void store_some(T* p, int64_t n, const float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < n) p[i] = narrow<T>(v[i]);
+template <int V, typename T>
+__device__ __forceinline__ void store_values(T* p, const T (&v)[V]) {
+  typename Values<T, V>::u r;
+  __builtin_memcpy(&r, v, sizeof r);
+  *reinterpret_cast<typename Values<T, V>::any*>(p) = r;
 }
 
-// use(eight values as they are stored, their place in the output, how many of them
-// are there) for the units [begin, end) of gradient j.
-template <typename T, typename Jobs, typename F>
-__device__ __forceinline__ void for_units(const ClipBatch<Jobs>& B, int j, int64_t begin, int64_t end, F&& use) {
+// use(V values as they are stored, their place in the output, how many of them are
+// there; zeros behind) for the units [begin, end) of gradient j.  Lanes take
+// neighbouring V, so that V of 16 bytes makes whole lines of each instruction.
+template <typename T, int V, typename Jobs, typename F>
+__device__ __forceinline__ void for_values(const ClipBatch<Jobs>& B, int j, int64_t begin, int64_t end, F&& use) {
   const T* g = reinterpret_cast<const T*>(B.job.g[j]);
   const int64_t cols = B.job.cols[j];
+  auto some = [&](const T* p, int64_t n, int64_t at) {
+    T v[V] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) v[i] = p[i];
+    use(v, at, n);
+  };
   if constexpr (Jobs::kRows) {
     const int64_t in_row = (cols + 7) / 8, all = B.job.rows[j] * in_row, ldg = B.job.ldg[j], ldo = B.job.ldo[j];
     if (end > all) end = all;
     for (int64_t u = begin + threadIdx.x; u < end; u += kThreads) {
-      const int64_t r = u / in_row, c = 8 * (u - r * in_row), n = cols - c;
-      const T* p = g + r * ldg + c;
-      use(n >= 8 ? load8<T>(p) : load_some<T>(p, n), r * ldo + c, n);
+      const int64_t r = u / in_row, c0 = 8 * (u - r * in_row);
+#pragma unroll
+      for (int64_t c = c0; c < c0 + 8; c += V) {
+        const T* p = g + r * ldg + c;
+        T v[V];
+        if (c + V <= cols) {
+          load_values<V>(p, v);
+          use(v, r * ldo + c, V);
+        } else if (c < cols) {
+          some(p, cols - c, r * ldo + c);
+        }
+      }
     }
   } else {
-    const int64_t whole = cols / 8;
-    const int64_t to = end < whole ? end : whole;
-    int64_t u = begin + threadIdx.x;
-    for (; u + (kAhead - 1) * kThreads < to; u += kAhead * kThreads) {
-      Raw8<T> r[kAhead];
+    const int64_t whole = cols / V * V, to = 8 * end < whole ? 8 * end : whole;
+    constexpr int64_t step = V * kThreads;
+    int64_t i = 8 * begin + V * (int64_t)threadIdx.x;
+    for (; i + (kAhead - 1) * step < to; i += kAhead * step) {
+      T v[kAhead][V];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) r[q] = load8<T>(g + 8 * (u + q * kThreads));
+      for (int q = 0; q < kAhead; ++q) load_values<V>(g + i + q * step, v[q]);
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) use(r[q], 8 * (u + q * kThreads), 8);
+      for (int q = 0; q < kAhead; ++q) use(v[q], i + q * step, V);
     }
-    for (; u < to; u += kThreads) use(load8<T>(g + 8 * u), 8 * u, 8);
-    if (whole >= begin && whole < end && threadIdx.x == 0 && cols > 8 * whole)
-      use(load_some<T>(g + 8 * whole, cols - 8 * whole), 8 * whole, cols - 8 * whole);
+    for (; i < to; i += step) {
+      T v[V];
+      load_values<V>(g + i, v);
+      use(v, i, V);
+    }
+    if (threadIdx.x == 0 && whole < cols && whole >= 8 * begin && whole < 8 * end) some(g + whole, cols - whole, whole);
   }
 }
 
 template <typename T, typename Jobs>
 __device__ __forceinline__ double squares_of(const ClipBatch<Jobs>& B, int j, int64_t begin, int64_t end) {
+  constexpr int V = 16 / sizeof(T);
   double s = 0.0, t = 0.0;
-  for_units<T>(B, j, begin, end, [&](const Raw8<T>& r, int64_t, int64_t) {
-    float v[8];
-    widen8(r, v);
+  for_values<T, V>(B, j, begin, end, [&](const T (&v)[V], int64_t, int64_t) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s = fma((double)v[i], (double)v[i], s);
-      t = fma((double)v[i + 1], (double)v[i + 1], t);
+    for (int i = 0; i < V; i += 2) {
+      const double a = (double)widen(v[i]), b = (double)widen(v[i + 1]);
+      s = fma(a, a, s);
+      t = fma(b, b, t);
     }
   });
   return s + t;
@@ -112,16 +133,19 @@ __device__ __forceinline__ double squares_of(const ClipBatch<Jobs>& B, int j, in
 
 template <typename T, typename O, typename Jobs>
 __device__ __forceinline__ void scale_to(const ClipBatch<Jobs>& B, int j, int64_t begin, int64_t end, double by) {
+  constexpr int V = 16 / sizeof(O);
   O* o = reinterpret_cast<O*>(B.job.out[j]);
-  for_units<T>(B, j, begin, end, [&](const Raw8<T>& r, int64_t at, int64_t n) {
-    float v[8];
-    widen8(r, v);
+  for_values<T, V>(B, j, begin, end, [&](const T (&v)[V], int64_t at, int64_t n) {
+    O w[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * by);
-    if (n >= 8)
-      store8<O>(o + at, v);
-    else
-      store_some<O>(o + at, n, v);
+    for (int i = 0; i < V; ++i) w[i] = narrow<O>((float)((double)widen(v[i]) * by));
+    if (n >= V) {
+      store_values<V>(o + at, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) o[at + i] = w[i];
+    }
   });
 }
 

@@ -23,56 +23,55 @@ namespace mr {
 
 namespace {
 
-__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
-template <int CTRL>
+// What the lane r places on along its row of 16 holds, in either direction.
+template <int R>
 __device__ __forceinline__ uint32_t ror(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | CTRL, 0xf, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | R, 0xf, 0xf, false);
 }
-__device__ __forceinline__ uint32_t min16(uint32_t v) {
-  v = umin(v, ror<8>(v));
-  v = umin(v, ror<4>(v));
-  v = umin(v, ror<2>(v));
-  return umin(v, ror<1>(v));
+template <int R>
+__device__ __forceinline__ float ror(float v) {
+  return __uint_as_float(ror<R>(__float_as_uint(v)));
 }
-__device__ __forceinline__ float sum16(float v) {
-  v += __uint_as_float(ror<8>(__float_as_uint(v)));
-  v += __uint_as_float(ror<4>(__float_as_uint(v)));
-  v += __uint_as_float(ror<2>(__float_as_uint(v)));
-  return v + __uint_as_float(ror<1>(__float_as_uint(v)));
+// What the lane R places back holds, 0 in a row's first R lanes.
+template <int R>
+__device__ __forceinline__ int shr(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x110 | R, 0xf, 0xf, false);
 }
+// Of numbers (no NaN), without the quieting that fmaxf and fminf add.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, __builtin_inff()); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -__builtin_inff()); }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
 // Over the LPT = 16 or 64 lanes of a token, in each of them.
+template <int LPT, typename V, typename F>
+__device__ __forceinline__ V over(V v, F&& f) {
+  v = f(v, ror<8>(v));
+  v = f(v, ror<4>(v));
+  v = f(v, ror<2>(v));
+  v = f(v, ror<1>(v));
+  if (LPT == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
 template <int LPT>
-__device__ __forceinline__ uint32_t max_of(uint32_t v) {
-  return LPT == 16 ? max16(v) : max64(v);
+__device__ __forceinline__ float max_of(float v) {
+  return over<LPT>(v, [](float a, float b) { return larger(a, b); });
 }
 template <int LPT>
 __device__ __forceinline__ uint32_t min_of(uint32_t v) {
-  v = min16(v);
-  if (LPT == 64) {
-    v = umin(v, (uint32_t)__shfl_xor((int)v, 16));
-    v = umin(v, (uint32_t)__shfl_xor((int)v, 32));
-  }
-  return v;
+  return over<LPT>(v, [](uint32_t a, uint32_t b) { return umin(a, b); });
 }
 template <int LPT>
 __device__ __forceinline__ float sum_of(float v) {
-  v = sum16(v);
-  if (LPT == 64) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-  }
-  return v;
+  return over<LPT>(v, [](float a, float b) { return a + b; });
 }
 
-// Unsigned numbers in the order of the values: -inf is 0 (never chosen), the
-// zeros are one value, NaN is the largest.
+// Unsigned numbers in the order of the values; the zeros are one.
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  const uint32_t k = (u >> 31) ? ~u : u | 0x80000000u;
-  return v != v ? 0xffffffffu : u == 0xff800000u ? 0u : k;
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+  return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
 // Four consecutive logits from column c, -inf behind the end.
@@ -121,58 +120,116 @@ __device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]
 // ---------------------------------------------------------------- routing
 // LPT lanes for each token, Q times four logits in each: columns 4 (lane + LPT q)
 // and the three behind.
+//
+// Up to eight choices by 16 lanes: with tau the k-th largest of the lanes' own
+// largest logits, k of a token's logits at least reach tau, so all chosen ones do.
+// They are few (about 11 of 384 for k = 8), go to LDS, one to each lane, and each
+// finds its place by comparing itself with the others.  Where more than 16 reach
+// tau (equal values), and for more choices, one is chosen after another: the
+// largest, its first place, which is then taken out.  16384 tokens of 384 float32
+// logits, k = 8: ROUTE_US us, one after another 18.0.
 template <typename T, int LPT, int Q>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
-  constexpr int TPB = 256 / LPT;
+  constexpr int TPB = 256 / LPT, N = 4 * Q;
+  constexpr float kInf = __builtin_inff();
+  __shared__ uint64_t reach[LPT == 16 ? TPB : 1][16];
   const int lane = threadIdx.x % LPT;
   for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.tokens; t0 += (int64_t)gridDim.x * TPB) {
     // lanes behind the last token work on that one and store nothing
     const bool held = t0 + threadIdx.x / LPT < a.tokens;
     const int64_t t = held ? t0 + threadIdx.x / LPT : a.tokens - 1;
     const T* row = reinterpret_cast<const T*>(a.logits) + t * a.ldl;
-    uint32_t key[4 * Q];
+    float v[N];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      float v[4];
-      load4<T>(row, 4 * (lane + LPT * q), a.n, v);
+      float u[4];
+      load4<T>(row, 4 * (lane + LPT * q), a.n, u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) key[4 * q + i] = key_of(v[i]);
+      for (int i = 0; i < 4; ++i) v[4 * q + i] = u[i] != u[i] ? kInf : u[i];
     }
-    float top = 0.f, all = 0.f, mine = 0.f;
+    auto largest = [&]() {
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) m = larger(m, v[i]);
+      return m;
+    };
+    const float own = largest(), top = max_of<LPT>(own);
+    float sum = 0.f;
+    if (!a.normalize) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += v[i] == -kInf ? 0.f : expf(v[i] - top);
+      sum = sum_of<LPT>(sum);
+    }
+    // of this lane: one of the chosen, which one of them, its share before the division
     int32_t expert = -1;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = key[0];
+    int place = lane;
+    float part = 0.f;
+    bool done = false;
+    if constexpr (LPT == 16) {
+      if (a.k <= 8) {
+        int above = 0;
+        static_for<15>([&](auto r) { above += ror<r.value + 1>(own) > own; });
+        float tau = over<16>(above < a.k ? own : kInf, [](float x, float y) { return smaller(x, y); });
+        tau = larger(tau, -3.402823466e38f);  // -inf is not chosen
+        int count = 0;
 #pragma unroll
-      for (int i = 1; i < 4 * Q; ++i) m = umax(m, key[i]);
-      m = max_of<LPT>(m);
-      if (j == 0) {
-        top = value_of(m);
-        if (!a.normalize) {
+        for (int i = 0; i < N; ++i) count += v[i] >= tau;
+        int upto = count;
+        upto += shr<1>(upto);
+        upto += shr<2>(upto);
+        upto += shr<4>(upto);
+        upto += shr<8>(upto);
+        const int total = over<16>((uint32_t)upto, [](uint32_t x, uint32_t y) { return umax(x, y); });
+        done = !__any(total > 16);
+        if (done) {
+          uint64_t* mine = reach[threadIdx.x / 16];
+          int at = upto - count;
 #pragma unroll
-          for (int i = 0; i < 4 * Q; ++i) all += key[i] ? expf(value_of(key[i]) - top) : 0.f;
+          for (int i = 0; i < N; ++i)
+            if (v[i] >= tau) mine[at++] = (uint64_t)key_of(v[i]) << 32 | ~(4u * lane + 64u * (i / 4) + i % 4);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          const uint64_t own_key = lane < total ? mine[lane] : 0;
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          place = 0;
+          const uint32_t hi = (uint32_t)(own_key >> 32), lo = (uint32_t)own_key;
+          static_for<15>([&](auto r) {
+            const uint64_t other = (uint64_t)ror<r.value + 1>(hi) << 32 | ror<r.value + 1>(lo);
+            place += other > own_key;
+          });
+          if (lane >= total) place = lane;  // behind the others
+          if (lane < total && place < a.k) {
+            expert = (int32_t)~lo;
+            const float value = __uint_as_float((hi >> 31) ? hi ^ 0x80000000u : ~hi);
+            part = expf(value - top);
+          }
         }
       }
-      // the first of the equal ones
-      uint32_t at = 0xffffffffu;
+    }
+    if (!done) {
+      place = lane;
+      for (int j = 0; j < a.k; ++j) {
+        const float m = max_of<LPT>(largest());
+        // the first of the equal ones
+        uint32_t at = 0xffffffffu;
 #pragma unroll
-      for (int i = 4 * Q - 1; i >= 0; --i) at = key[i] == m ? 4u * LPT * (i / 4) + i % 4 : at;
-      at = at == 0xffffffffu ? at : at + 4u * lane;
-      at = min_of<LPT>(at);
-      const uint32_t here = at - 4u * lane;
+        for (int i = N - 1; i >= 0; --i) at = v[i] == m ? 4u * LPT * (i / 4) + i % 4 : at;
+        at = min_of<LPT>(at == 0xffffffffu ? at : at + 4u * lane);
+        const uint32_t here = at - 4u * lane;
 #pragma unroll
-      for (int i = 0; i < 4 * Q; ++i) key[i] = here == 4u * LPT * (i / 4) + i % 4 ? 0u : key[i];
-      if (lane == j && m) {
-        expert = (int32_t)at;
-        mine = expf(value_of(m) - top);
+        for (int i = 0; i < N; ++i) v[i] = here == 4u * LPT * (i / 4) + i % 4 ? -kInf : v[i];
+        if (lane == j && m > -kInf) {
+          expert = (int32_t)at;
+          part = expf(m - top);
+        }
       }
     }
-    const float sum = sum_of<LPT>(a.normalize ? mine : all);
+    if (a.normalize) sum = sum_of<LPT>(part);
     if (!held) continue;
-    if (lane < a.k) {
-      a.experts[t * a.k + lane] = expert;
-      a.weights[t * a.k + lane] = expert < 0 ? 0.f : mine / sum;
+    if (place < a.k) {
+      a.experts[t * a.k + place] = expert;
+      a.weights[t * a.k + place] = expert < 0 ? 0.f : part / sum;
     }
-    if (lane == 0) a.log_sum[t] = expert < 0 ? -__builtin_inff() : top + logf(sum);
+    if (lane == 0) a.log_sum[t] = top == -kInf ? top : top + logf(sum);
   }
 }
 
@@ -216,7 +273,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) 
       }
       sum = sum64(sum);
     }
-    const float c = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(sum16(w * dw))));
+    const float c = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(sum_of<16>(w * dw))));
     const float part = a.normalize ? w * (dw - c) : w * dw;
     const float share = sum == 0.f ? 0.f : c / sum;
     for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {

@@ -276,6 +276,7 @@ def fake(monkeypatch):
         monkeypatch.setattr(module, "_in_use_on", lambda stream, *t: used.append((stream, [x for x in t if x is not None])))
     monkeypatch.setattr(B, "library", lambda: lib)
     monkeypatch.setattr(B, "_stream", lambda stream: 0)
+    monkeypatch.setattr(B, "_current_gpu", lambda: -1)
     monkeypatch.setattr(B, "_in_use_on", lambda stream, *t: used.append((stream, [x for x in t if x is not None])))
     lib.used = used
     return lib
@@ -347,6 +348,13 @@ def test_what_does_not_fit_is_refused(fake):
         with pytest.raises(ValueError):
             call()
             raise AssertionError(f"refusal {i} passed")
+    assert fake.calls == []
+
+
+def test_gradients_of_another_device_are_refused(fake, monkeypatch):
+    monkeypatch.setattr(B, "_current_gpu", lambda: 0)
+    with pytest.raises(ValueError, match="current GPU"):
+        B.clip_gradients_batched([torch.zeros(4)], 1.0)
     assert fake.calls == []
 
 

@@ -54,6 +54,7 @@ def streams(monkeypatch):
     for module in (B, L, X):
         monkeypatch.setattr(module, "library", lambda: FakeLib())
         monkeypatch.setattr(module, "_in_use_on", mark)
+    monkeypatch.setattr(B, "_current_gpu", lambda: -1)
     for module in (L, X):
         monkeypatch.setattr(module, "_device", lambda *t: torch.device("cpu"))
         monkeypatch.setattr(module, "_stream", lambda stream, dev: 0)
