@@ -74,24 +74,55 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Four consecutive logits from column c, -inf behind the end.
+// Q times four consecutive logits of a row, from columns c, c + step, ..; -inf
+// behind its end.  All loads come before the first use and without a branch that
+// lanes take apart: lanes at the end load the row's last four and move them down (rows of one to three
+// go to all lanes, and count for the first).
 template <typename T>
-__device__ __forceinline__ void load4(const T* row, int c, int n, float (&v)[4]) {
-  if (c + 4 <= n) {
-    T t[4];
-    if constexpr (sizeof(T) == 4) {
-      const v4u u = *reinterpret_cast<const v4u_any*>(row + c);
-      __builtin_memcpy(t, &u, 16);
-    } else {
-      const v2u u = *reinterpret_cast<const v2u_any*>(row + c);
-      __builtin_memcpy(t, &u, 8);
+struct Raw4 {
+  typedef uint32_t u __attribute__((ext_vector_type(sizeof(T))));
+  typedef u any __attribute__((aligned(1)));
+};
+__device__ __forceinline__ float widen_of(const v4u& r, int i, float) { return __uint_as_float(r[i]); }
+__device__ __forceinline__ float widen_of(const v2u& r, int i, bf16_t) {
+  return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+}
+__device__ __forceinline__ float widen_of(const v2u& r, int i, _Float16) {
+  const uint16_t h = (uint16_t)(i & 1 ? r[i >> 1] >> 16 : r[i >> 1]);
+  _Float16 f;
+  __builtin_memcpy(&f, &h, 2);
+  return (float)f;
+}
+template <typename T, int Q>
+__device__ __forceinline__ void load_logits(const T* row, int c, int step, int n, float (&v)[4 * Q]) {
+  if (n >= 4) {
+    typename Raw4<T>::u r[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int at = c + q * step;
+      r[q] = *reinterpret_cast<const typename Raw4<T>::any*>(row + (at + 4 <= n ? at : n - 4));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = widen(t[i]);
-    return;
+    for (int i = 0; i < 4 * Q; ++i) v[i] = widen_of(r[i / 4], i % 4, T());
+    if (n & 3) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int s = c + q * step + 4 - n;
+        const bool one = s > 0 && (s & 1), two = s > 0 && (s & 2);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[4 * q + i] = one ? v[4 * q + i + 1] : v[4 * q + i];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[4 * q + i] = two ? v[4 * q + i + 2] : v[4 * q + i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * Q; ++i) v[i] = i < 3 ? widen(row[i < n ? i : 0]) : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = c + i < n ? widen(row[c + i]) : -__builtin_inff();
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * q + i] = c + q * step + i < n ? v[4 * q + i] : -__builtin_inff();
 }
 template <typename T>
 __device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]) {
@@ -140,13 +171,9 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
     const int64_t t = held ? t0 + threadIdx.x / LPT : a.tokens - 1;
     const T* row = reinterpret_cast<const T*>(a.logits) + t * a.ldl;
     float v[N];
+    load_logits<T, Q>(row, 4 * lane, 4 * LPT, a.n, v);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      float u[4];
-      load4<T>(row, 4 * (lane + LPT * q), a.n, u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] = u[i] != u[i] ? kInf : u[i];
-    }
+    for (int i = 0; i < N; ++i) v[i] = v[i] != v[i] ? kInf : v[i];
     auto largest = [&]() {
       float m = v[0];
 #pragma unroll
@@ -257,14 +284,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) 
     float v[4], top = -__builtin_inff(), sum = 0.f;
     if (!a.normalize) {
       for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {
-        load4<T>(row, c0 + 4 * lane, a.n, v);
+        load_logits<T, 1>(row, c0 + 4 * lane, 0, a.n, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i]);
       }
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
       for (int c0 = 0; c0 < (ONE ? 1 : a.n); c0 += 256) {
-        if (!ONE) load4<T>(row, c0 + 4 * lane, a.n, v);
+        if (!ONE) load_logits<T, 1>(row, c0 + 4 * lane, 0, a.n, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[i] = v[i] == -__builtin_inff() ? 0.f : expf(v[i] - top);
@@ -281,7 +308,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) 
       float d[4] = {0.f, 0.f, 0.f, 0.f};
       if (!a.normalize) {
         if (!ONE) {
-          load4<T>(row, col, a.n, v);
+          load_logits<T, 1>(row, col, 0, a.n, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = v[i] == -__builtin_inff() ? 0.f : expf(v[i] - top);
         }
