@@ -330,7 +330,12 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouteGradArgs a) 
 // ------------------------------------------------------------------ order
 namespace {
 
-constexpr int kRound = 4;
+// Choices of a lane in a round.  All of a few thousand in one workgroup's only
+// round spare a launch (4096 choices: 6.5 us, in two launches 8.0); more are
+// shared out thinly, as a workgroup's waves wait for one another (131072 choices
+// of 64 and of 384 experts: 9.1 and 12.1 us with two, 11.1 and 12.7 with four, 8.6
+// and 13.7 with one).
+constexpr int kAlone = 4, kShared = 2;
 
 // Expert of choice f, n where it is none.
 __device__ __forceinline__ int choice(const OrderArgs& a, int f) {
@@ -370,11 +375,12 @@ __device__ __forceinline__ void exclusive_sums(int32_t* v, int n, int32_t* waves
 
 }  // namespace
 
-// The places of a workgroup's choices, in rounds of kRound for each lane.  In a
-// round each wave takes the next 64 kRound: lanes of one expert find each other by
+// The places of a workgroup's choices, in rounds of R for each lane.  In a
+// round each wave takes the next 64 R: lanes of one expert find each other by
 // the bits of its number, the first of them keeps the wave's count.  With one
 // workgroup, and one round, the places are final; else they count from the
 // expert's first row of this workgroup, and order_place_kernel adds where that is.
+template <int R>
 __global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
   extern __shared__ int32_t lds[];  // waves x bins counts, bins totals, 16 for the scan
   const int bins = a.n + 1, waves = blockDim.x >> 6;
@@ -383,18 +389,18 @@ __global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
   int32_t* total = lds + waves * bins;
   const int64_t begin = (int64_t)blockIdx.x * a.chunk;
   const int64_t end = begin + a.chunk < a.total ? begin + a.chunk : a.total;
-  const int round = (int)blockDim.x * kRound;
+  const int round = (int)blockDim.x * R;
   int64_t f = end;
-  int e[kRound], rank[kRound];
+  int e[R], rank[R];
   for (int i = threadIdx.x; i < bins; i += blockDim.x) total[i] = 0;
   for (int64_t f0 = begin; f0 < end; f0 += round) {
-    f = f0 + wave * 64 * kRound + lane;
+    f = f0 + wave * 64 * R + lane;
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) e[r] = f + 64 * r < end ? choice(a, (int)(f + 64 * r)) : a.n;
+    for (int r = 0; r < R; ++r) e[r] = f + 64 * r < end ? choice(a, (int)(f + 64 * r)) : a.n;
     for (int i = threadIdx.x; i < waves * bins; i += blockDim.x) lds[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) {
+    for (int r = 0; r < R; ++r) {
       const bool valid = f + 64 * r < end;
       uint64_t same = __ballot(valid);
       for (int b = 0; (bins - 1) >> b; ++b) {
@@ -425,7 +431,7 @@ __global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
     __syncthreads();
     if (!a.counts) break;  // one workgroup has one round
 #pragma unroll
-    for (int r = 0; r < kRound; ++r)
+    for (int r = 0; r < R; ++r)
       if (f + 64 * r < end) a.place[f + 64 * r] = rank[r] + count[e[r]];
     __syncthreads();
   }
@@ -437,7 +443,7 @@ __global__ __launch_bounds__(1024) void order_rank_kernel(const OrderArgs a) {
   exclusive_sums(total, bins, total + bins);
   for (int i = threadIdx.x; i < bins; i += blockDim.x) a.offsets[i] = total[i];
 #pragma unroll
-  for (int r = 0; r < kRound; ++r)
+  for (int r = 0; r < R; ++r)
     if (f + 64 * r < end) a.place[f + 64 * r] = rank[r] + count[e[r]] + total[e[r]];
 }
 
@@ -470,16 +476,16 @@ __global__ __launch_bounds__(1024) void order_place_kernel(const OrderArgs a) {
     for (int e = threadIdx.x; e < bins; e += blockDim.x) a.offsets[e] = total[e];
   const int64_t begin = (int64_t)blockIdx.x * a.chunk;
   const int64_t end = begin + a.chunk < a.total ? begin + a.chunk : a.total;
-  for (int64_t f = begin + threadIdx.x; f < end; f += blockDim.x * kRound) {
-    int e[kRound], p[kRound];
+  for (int64_t f = begin + threadIdx.x; f < end; f += blockDim.x * kShared) {
+    int e[kShared], p[kShared];
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) {
+    for (int r = 0; r < kShared; ++r) {
       const int64_t g = f + (int64_t)blockDim.x * r;
       e[r] = g < end ? choice(a, (int)g) : 0;
       p[r] = g < end ? a.place[g] : 0;
     }
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) {
+    for (int r = 0; r < kShared; ++r) {
       const int64_t g = f + (int64_t)blockDim.x * r;
       if (g < end) a.place[g] = p[r] + total[e[r]] + before[e[r]];
     }
@@ -733,18 +739,25 @@ hipError_t launch_route_grad(const RouteGradArgs& a, mr_dtype dt, hipStream_t s)
 void order_plan(int64_t total, int64_t n, int32_t* chunk, int32_t* blocks, int32_t* waves) {
   // counts of every wave in 64 KB of LDS
   *waves = n < 900 ? 16 : n < 1800 ? 8 : n < 3000 ? 4 : 2;
-  const int64_t round = 64 * kRound * *waves;
-  int64_t c = round;
-  while ((total + c - 1) / c > 256) c *= 2;  // every workgroup reads all workgroups' counts
+  int64_t c = 64 * kAlone * *waves;
+  if (total > c) {
+    c = 64 * kShared * *waves;
+    while ((total + c - 1) / c > 256) c *= 2;  // every workgroup reads all workgroups' counts
+  }
   *chunk = (int32_t)c;
   *blocks = total > c ? (int32_t)((total + c - 1) / c) : 1;
 }
 
 hipError_t launch_order(const OrderArgs& a, hipStream_t s) {
   const size_t bins = (size_t)a.n + 1;
-  hipLaunchKernelGGL(order_rank_kernel, dim3(a.blocks), dim3(64 * a.waves), (bins * (a.waves + 1) + 16) * 4, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.counts) return e;
+  const size_t lds = (bins * (a.waves + 1) + 16) * 4;
+  if (!a.counts) {
+    hipLaunchKernelGGL(order_rank_kernel<kAlone>, dim3(1), dim3(64 * a.waves), lds, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(order_rank_kernel<kShared>, dim3(a.blocks), dim3(64 * a.waves), lds, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(order_place_kernel, dim3(a.blocks), dim3(1024), (bins * 2 + 16) * 4, s, a);
   return hipGetLastError();
 }
