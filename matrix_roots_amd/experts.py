@@ -43,7 +43,7 @@ def _matrix(name, t):
 
 def _small(name, t, shape, dtype):
     """A contiguous array of 4-byte values."""
-    _same_shape(name, t, torch.Size(shape))
+    _same_shape(name, t, shape)
     if t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype}")
 
@@ -53,10 +53,11 @@ def _experts_of(order, tokens) -> tuple:
     offsets, place = order
     if place.dim() != 2 or place.shape[0] != tokens:
         raise ValueError("the order is for another number of tokens")
-    _small("order.place", place, place.shape, torch.int32)
     if offsets.dim() != 1:
         raise ValueError("order.offsets must be a vector")
-    _small("order.offsets", offsets, offsets.shape, torch.int32)
+    for t in order:
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("an order is contiguous int32")
     return offsets.shape[0] - 1, place.shape[1]
 
 
