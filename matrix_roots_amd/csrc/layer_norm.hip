@@ -36,9 +36,76 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float (*red)[16]) {
   for (int w = 1; w < TPR / 64; ++w) u += red[0][w], v += red[1][w];
 }
 
+// The eight columns a thread holds of a row in chunk k of CH.  Chunks before the
+// last are whole (`pick` takes the smallest CH).  In that one the thread at a ragged
+// end takes the row's last eight, and threads behind it do too: all loads are
+// whole and none depends on a branch.  The columns that a neighbour holds as well,
+// the first `skip`, are left out of the row's sums; what is stored for them twice is
+// the same.  Rows of less than eight (FEW) are the first thread's.
+template <int TPR, int CH, bool FEW>
+struct Span {
+  int c, skip, width;
+  __device__ __forceinline__ Span(int t, int k, int w) : width(w) {
+    const int at = chunk_col<TPR>(t, k);
+    c = FEW ? 0 : k < CH - 1 || at + 8 <= w ? at : w - 8;
+    skip = FEW ? (t == 0 ? 0 : 8) : at - c;
+  }
+  __device__ __forceinline__ bool mine(int i) const { return i >= skip && (!FEW || i < width); }
+  __device__ __forceinline__ bool any() const { return skip < 8; }
+  template <typename T>
+  __device__ __forceinline__ Raw8<T> load(const T* row) const {
+    if constexpr (!FEW) return load8<T>(row + c);
+    T v[8] = {};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < width) v[i] = row[i];
+    Raw8<T> r;
+    __builtin_memcpy(&r, v, sizeof r);
+    return r;
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, const float (&v)[8]) const {
+    if (!any()) return;
+    if constexpr (!FEW) {
+      store8<T>(row + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < width) row[i] = narrow<T>(v[i]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void param(const void* p, int f32, float (&v)[8]) const {
+    if (f32)
+      widen8(load<float>(reinterpret_cast<const float*>(p)), v);
+    else
+      widen8(load<T>(reinterpret_cast<const T*>(p)), v);
+  }
+  // v in 8 bits with its block's scale; q and s are the row's.  All 64 lanes take part.
+  __device__ __forceinline__ void store_eight(unsigned char* q, float* s, const float (&v)[8], bool e5m2) const {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = mine(i) ? umax(amax, magnitude(v[i])) : amax;
+    amax = max16(amax);
+    const float sb = block_scale(amax, e5m2);
+    const Quotient over(sb);
+    if (any() && (threadIdx.x & 15) == 0) s[(c + skip) / kBlock] = sb;
+    v2u p;
+    p[0] = pack4(over(v[0]), over(v[1]), over(v[2]), over(v[3]), e5m2);
+    p[1] = pack4(over(v[4]), over(v[5]), over(v[6]), over(v[7]), e5m2);
+    if (!FEW && skip == 0) {
+      *reinterpret_cast<v2u_any*>(q + c) = p;
+    } else if (any()) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (mine(i)) q[c + i] = (unsigned char)(p[i >> 2] >> (8 * (i & 3)));
+    }
+  }
+};
+
 }  // namespace
 
-template <typename T, int TPR, int CH>
+template <typename T, int TPR, int CH, bool FEW>
 __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(const LayerNormArgs a) {
   __shared__ float red[2][16];
   constexpr int RPB = kNormThreads<TPR> / TPR, NV = 8;
@@ -50,37 +117,61 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
     if (TPR == 64 && r >= a.rows) break;  // whole waves: no barrier follows
     const T* x = reinterpret_cast<const T*>(a.x) + r * a.ldx;
     const T* res = a.res ? reinterpret_cast<const T*>(a.res) + r * a.ldres : nullptr;
+    auto span = [&](int k) { return Span<TPR, CH, FEW>(t, k, a.width); };
+    Raw8<T> raw[CH];
     float v[CH][NV];
 #pragma unroll
-    for (int k = 0; k < CH; ++k) load_chunk<T>(x, chunk_col<TPR>(t, k), a.width, v[k]);
+    for (int k = 0; k < CH; ++k) raw[k] = span(k).load(x);
     if (res) {
       T* h = reinterpret_cast<T*>(a.h) + r * a.ldh;
-      float u[CH][NV];
+      Raw8<T> add[CH];
 #pragma unroll
-      for (int k = 0; k < CH; ++k) load_chunk<T>(res, chunk_col<TPR>(t, k), a.width, u[k]);
+      for (int k = 0; k < CH; ++k) add[k] = span(k).load(res);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
+        float u[NV];
+        widen8(raw[k], v[k]);
+        widen8(add[k], u);
         // the stored sum, rounded to T, is what the norm is of: the backward pass reads it
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[k][i] = widen(narrow<T>(v[k][i] + u[k][i]));
-        store_chunk<T>(h, chunk_col<TPR>(t, k), a.width, v[k]);
+        for (int i = 0; i < NV; ++i) v[k][i] = widen(narrow<T>(v[k][i] + u[i]));
+        span(k).store(h, v[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) widen8(raw[k], v[k]);
     }
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+    for (int k = 0; k < CH; ++k) {
+      if (k == CH - 1) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s += v[k][i];
-    const float m = row_sum<TPR>(s, red[0]) * inv_width;
+        for (int i = 0; i < NV; ++i) s += span(k).mine(i) ? v[k][i] : 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += v[k][i];
+      }
+    }
+    float m = row_sum<TPR>(s, red[0]) * inv_width;
+    asm volatile("" : "+v"(m));  // one rounded m for all differences: none takes the product in a fused operation
     float ds = 0.f, ss = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = chunk_col<TPR>(t, k);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[k][i] = c + i < a.width ? v[k][i] - m : 0.f;
-        ds += v[k][i];
-        ss = fmaf(v[k][i], v[k][i], ss);
+      for (int i = 0; i < NV; ++i) v[k][i] -= m;
+      if (k == CH - 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float d = span(k).mine(i) ? v[k][i] : 0.f;
+          ds += d;
+          ss = fmaf(d, d, ss);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          ds += v[k][i];
+          ss = fmaf(v[k][i], v[k][i], ss);
+        }
       }
     }
     row_sum2<TPR>(ds, ss, red);
@@ -92,36 +183,23 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = chunk_col<TPR>(t, k);
       float w[NV], b[NV];
-      load_param<T>(a.w, a.w_f32, c, a.width, w);
+      span(k).template param<T>(a.w, a.w_f32, w);
 #pragma unroll
       for (int i = 0; i < NV; ++i) b[i] = 0.f;
-      if (a.b) load_param<T>(a.b, a.w_f32, c, a.width, b);
+      if (a.b) span(k).template param<T>(a.b, a.w_f32, b);
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[k][i] = fmaf((v[k][i] - e) * rho, w[i], b[i]);
-      if (a.y) store_chunk<T>(reinterpret_cast<T*>(a.y) + r * a.ldy, c, a.width, v[k]);
-      if (a.q) store_eight(a.q + r * a.ldq, a.s + r * a.lds, c, a.width, v[k], a.e5m2);  // 0 behind the row's end
+      if (a.y) span(k).store(reinterpret_cast<T*>(a.y) + r * a.ldy, v[k]);
+      if (a.q) span(k).store_eight(a.q + r * a.ldq, a.s + r * a.lds, v[k], a.e5m2);
     }
   }
 }
 
-// A row's eight values of a chunk as they are stored, 0 behind its end.
-template <typename T>
-__device__ __forceinline__ Raw8<T> raw_chunk(const T* row, int c, int width) {
-  if (c + 8 <= width) return load8<T>(row + c);
-  T t[8] = {};
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (c + i < width) t[i] = row[c + i];
-  Raw8<T> r;
-  __builtin_memcpy(&r, t, sizeof r);
-  return r;
-}
-
 // Rows r0, r0 + gridDim RPB, ...: dx, and this workgroup's column sums of dy hh
-// and of dy into a.partial[2 blockIdx.x] and the row behind it.
-template <typename T, int TPR, int CH>
+// and of dy into a.partial[2 blockIdx.x] and the row behind it.  Rows stay as they
+// are stored until they are used, which leaves registers for the next row's loads.
+template <typename T, int TPR, int CH, bool FEW>
 __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(const LayerNormArgs a) {
   constexpr int RPB = kNormThreads<TPR> / TPR, NV = 8;
   __shared__ float red[2][16];
@@ -138,14 +216,15 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
   const int64_t step = (int64_t)gridDim.x * RPB;
   // the next row's loads are under way while one is worked on, but for the widest of float32, which takes all registers
   constexpr bool kAhead = sizeof(T) == 2 || TPR < 512;
+  auto span = [&](int k) { return Span<TPR, CH, FEW>(t, k, a.width); };
   auto load = [&](int64_t r) {
     const T* from_dy = reinterpret_cast<const T*>(a.dy) + r * a.lddy;
     const T* from_h = reinterpret_cast<const T*>(a.x) + r * a.ldx;
     rho = a.rstd_in[r], mu = a.mean_in[r];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      dy[k] = raw_chunk<T>(from_dy, chunk_col<TPR>(t, k), a.width);
-      h[k] = raw_chunk<T>(from_h, chunk_col<TPR>(t, k), a.width);
+      dy[k] = span(k).load(from_dy);
+      h[k] = span(k).load(from_h);
     }
   };
   int64_t r = (int64_t)blockIdx.x * RPB + (RPB == 1 ? 0 : threadIdx.x / TPR);
@@ -159,13 +238,13 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       now_dy[k] = dy[k], now_h[k] = h[k];
-      if (res) rr[k] = raw_chunk<T>(res, chunk_col<TPR>(t, k), a.width);
+      if (res) rr[k] = span(k).load(res);
     }
     if (kAhead && r + step < a.rows) load(r + step);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float w[NV], g[NV], hh[NV];
-      load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
+      span(k).template param<T>(a.w, a.w_f32, w);
       widen8(now_dy[k], g);
       widen8(now_h[k], hh);
 #pragma unroll
@@ -173,9 +252,21 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
         hh[i] = (hh[i] - now_mu) * now_rho;
         dw[k][i] = fmaf(g[i], hh[i], dw[k][i]);
         db[k][i] += g[i];
-        g[i] *= w[i];  // 0 behind the row's end
-        sg += g[i];
-        dot = fmaf(g[i], hh[i], dot);
+        g[i] *= w[i];
+      }
+      if (k == CH - 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const bool in = span(k).mine(i);
+          sg += in ? g[i] : 0.f;
+          dot += in ? g[i] * hh[i] : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          sg += g[i];
+          dot = fmaf(g[i], hh[i], dot);
+        }
       }
     }
     row_sum2<TPR>(sg, dot, red);
@@ -184,7 +275,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float w[NV], g[NV], hh[NV], u[NV];
-      load_param<T>(a.w, a.w_f32, chunk_col<TPR>(t, k), a.width, w);
+      span(k).template param<T>(a.w, a.w_f32, w);
       widen8(now_dy[k], g);
       widen8(now_h[k], hh);
 #pragma unroll
@@ -192,7 +283,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
       if (res) widen8(rr[k], u);
 #pragma unroll
       for (int i = 0; i < NV; ++i) u[i] += now_rho * (g[i] * w[i] - c0 - (hh[i] - now_mu) * now_rho * c1);
-      store_chunk<T>(dx, chunk_col<TPR>(t, k), a.width, u);
+      span(k).store(dx, u);
     }
     if (!kAhead && r + step < a.rows) load(r + step);
     r += step;
@@ -221,8 +312,8 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
   }
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    store_chunk<float>(out, chunk_col<TPR>(t, k), a.width, dw[k]);
-    store_chunk<float>(out + a.width, chunk_col<TPR>(t, k), a.width, db[k]);
+    span(k).store(out, dw[k]);
+    span(k).store(out + a.width, db[k]);
   }
 }
 
@@ -256,23 +347,27 @@ namespace {
 
 constexpr int kMaxBlocks = 2048;  // 8 workgroups per CU
 
-template <typename T, int TPR, int CH>
+template <typename T, int TPR, int CH, bool FEW = false>
 hipError_t go(const LayerNormArgs& a, bool backward, int blocks, hipStream_t s) {
   if (backward)
-    hipLaunchKernelGGL((layer_norm_backward_kernel<T, TPR, CH>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_backward_kernel<T, TPR, CH, FEW>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
   else
-    hipLaunchKernelGGL((layer_norm_forward_kernel<T, TPR, CH>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_forward_kernel<T, TPR, CH, FEW>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t pick(const LayerNormArgs& a, bool backward, int blocks, hipStream_t s) {
   const int w = a.width;
+  if (w < 8) return go<T, 64, 1, true>(a, backward, blocks, s);
   if (w <= 512) return go<T, 64, 1>(a, backward, blocks, s);
   if (w <= 1024) return go<T, 64, 2>(a, backward, blocks, s);
+  if (w <= 1536) return go<T, 64, 3>(a, backward, blocks, s);
   if (w <= 2048) return go<T, 64, 4>(a, backward, blocks, s);
   if (w <= 4096) return go<T, 256, 2>(a, backward, blocks, s);
+  if (w <= 6144) return go<T, 256, 3>(a, backward, blocks, s);
   if (w <= 8192) return go<T, 256, 4>(a, backward, blocks, s);
+  if (w <= 12288) return go<T, 512, 3>(a, backward, blocks, s);
   return go<T, 512, 4>(a, backward, blocks, s);
 }
 

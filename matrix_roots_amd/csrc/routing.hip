@@ -500,173 +500,192 @@ __device__ __forceinline__ int64_t held_rows(const RowsArgs& a, int64_t rows) {
   const int64_t h = a.offsets[a.experts];
   return h < 0 ? 0 : h < rows ? h : rows;
 }
-template <typename T>
-__device__ __forceinline__ void load_part(const T* row, int c, int width, float (&v)[8]) {
-  if (c + 8 <= width) {
-    widen8(load8<T>(row + c), v);
-    return;
+
+// Eight columns from `at` of a row.  At a ragged end they are the row's last eight,
+// so that no load or store is taken apart; the first `skip` of them are a
+// neighbour's too, which stores the same there.  Rows of less than eight (FEW)
+// have one such part.
+template <typename T, bool FEW>
+struct Part {
+  int c, skip, width;
+  __device__ __forceinline__ Part(int at, int w) : width(w) {
+    c = FEW ? 0 : at + 8 <= w ? at : w - 8;
+    skip = FEW ? (at == 0 ? 0 : 8) : at - c;
   }
+  __device__ __forceinline__ bool any() const { return skip < 8; }
+  __device__ __forceinline__ Raw8<T> load(const T* row) const {
+    if constexpr (!FEW) return load8<T>(row + c);
+    T v[8] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (c + i < width) v[i] = widen(row[c + i]);
-}
-template <typename T>
-__device__ __forceinline__ void store_part(T* row, int c, int width, const float (&v)[8]) {
-  if (c + 8 <= width) {
-    store8<T>(row + c, v);
-    return;
+    for (int i = 0; i < 7; ++i)
+      if (i < width) v[i] = row[i];
+    Raw8<T> r;
+    __builtin_memcpy(&r, v, sizeof r);
+    return r;
   }
+  __device__ __forceinline__ void store(T* row, const Raw8<T>& r) const {
+    if constexpr (!FEW) {
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (c + i < width) row[c + i] = narrow<T>(v[i]);
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<v4u_any*>(row + c)[i] = r.u[i];
+    } else {
+      T v[8];
+      __builtin_memcpy(v, &r, sizeof r);
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < width) row[i] = v[i];
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> narrow8(const float (&v)[8]) {
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = narrow<T>(v[i]);
+  Raw8<T> r;
+  __builtin_memcpy(&r, t, sizeof r);
+  return r;
 }
 
-constexpr int kPart = 512;  // columns that a wave holds 8 of in each lane
+// Combined rows go in parts of 128 columns, 16 lanes of eight each; the parts of a row
+// are neighbours, so that a wave's four are 512 columns of a wide row or four rows.
+constexpr int kPartLanes = 16, kPart = 8 * kPartLanes;
+constexpr int kChoices = 4;  // of a token, in flight together
+
+// The job of the thread's 16 lanes: part `part` of token t, or t past the end.
+__device__ __forceinline__ void part_of(int64_t job, int64_t jobs, int parts, int64_t& t, int& part) {
+  t = jobs >> 31 ? job / parts : (int)job / parts;
+  part = (int)(job - t * parts);
+}
 
 }  // namespace
 
-// A wave for each token and 4 parts of its row: to the places of its choices.
-template <typename T>
+// To the places of a token's choices.  LPR = 16 or 64 lanes, CH parts of eight columns
+// in each, for a piece of its row: wide rows go out in pieces of 4 KB (16384 x 8
+// rows of 2048 bf16: 92 us from a clean cache, in pieces of 256 bytes 105).
+template <typename T, int LPR, int CH, bool FEW>
 __global__ __launch_bounds__(256) void dispatch_kernel(const RowsArgs a) {
-  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
-  const int lane = threadIdx.x & 63;
+  constexpr int GPB = 256 / LPR, kPiece = 8 * LPR * CH;
   const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
-  const int c0 = blockIdx.y * CH * kPart + 8 * lane;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
-    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ldx;
-    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
-    float v[CH][8];
+  const int parts = (a.width + kPiece - 1) / kPiece;
+  const int64_t jobs = a.tokens * parts;
+  for (int64_t job = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR; job < jobs; job += (int64_t)gridDim.x * GPB) {
+    int64_t t;
+    int part;
+    part_of(job, jobs, parts, t, part);
+    const int32_t* place = a.place + t * a.k;
+    const int c0 = part * kPiece + 8 * (int)(threadIdx.x % LPR);
+    Raw8<T> v[CH];
 #pragma unroll
-    for (int q = 0; q < CH; ++q) load_part<T>(x, c0 + q * kPart, a.width, v[q]);
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t p = __builtin_amdgcn_readlane(mine, j);
-      if (p < 0 || p >= rows) continue;
-      T* y = reinterpret_cast<T*>(a.out) + p * a.ldo;
-      if (p < held) {
+    for (int q = 0; q < CH; ++q) v[q] = Part<T, FEW>(c0 + 8 * LPR * q, a.width).load(reinterpret_cast<const T*>(a.x) + t * a.ldx);
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      int64_t p[kChoices];
 #pragma unroll
-        for (int q = 0; q < CH; ++q) store_part<T>(y, c0 + q * kPart, a.width, v[q]);
-      } else {
-        const float zero[8] = {};
+      for (int i = 0; i < kChoices; ++i) p[i] = place[j0 + i < a.k ? j0 + i : j0];
 #pragma unroll
-        for (int q = 0; q < CH; ++q) store_part<T>(y, c0 + q * kPart, a.width, zero);
-      }
-    }
-  }
-}
-
-// A wave for each token: its row times the weights to the places of its choices,
-// and its dot products with the rows that lie there.
-template <typename T>
-__global__ __launch_bounds__(256) void dispatch_dot_kernel(const RowsArgs a) {
-  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
-  const int lane = threadIdx.x & 63;
-  const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
-    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ldx;
-    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
-    const float weight = lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
-    float dot = 0.f;
-    for (int c0 = 8 * lane; c0 - 8 * lane < a.width; c0 += CH * kPart) {
-      float v[CH][8];
-#pragma unroll
-      for (int q = 0; q < CH; ++q) load_part<T>(x, c0 + q * kPart, a.width, v[q]);
-      for (int j = 0; j < a.k; ++j) {
-        const int64_t p = __builtin_amdgcn_readlane(mine, j);
-        if (p < 0 || p >= rows) continue;
-        T* y = reinterpret_cast<T*>(a.out) + p * a.ldo;
-        const bool in = p < held;
-        const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
-        float s = 0.f;
-        if (in) {
-          const T* z = reinterpret_cast<const T*>(a.rows) + p * a.ldr;
-          float u[CH][8];
-#pragma unroll
-          for (int q = 0; q < CH; ++q) load_part<T>(z, c0 + q * kPart, a.width, u[q]);
-#pragma unroll
-          for (int q = 0; q < CH; ++q)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(u[q][i], v[q][i], s);
-        }
-        s = sum64(s);
-        dot += lane == j ? s : 0.f;
+      for (int i = 0; i < kChoices; ++i) {
+        if (j0 + i >= a.k || p[i] < 0 || p[i] >= rows) continue;
+        T* y = reinterpret_cast<T*>(a.out) + p[i] * a.ldo;
 #pragma unroll
         for (int q = 0; q < CH; ++q) {
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = in ? w * v[q][i] : 0.f;
-          store_part<T>(y, c0 + q * kPart, a.width, o);
+          const Part<T, FEW> at(c0 + 8 * LPR * q, a.width);
+          if (at.any()) at.store(y, p[i] < held ? v[q] : Raw8<T>{});
         }
       }
     }
-    if (lane < a.k) a.dots[t * a.k + lane] = dot;
   }
 }
 
-// A wave for each token and part of its row: its choices that an expert has, in
+// LPR = 16 or 64 lanes for each choice, CH parts of eight columns in each at a time:
+// the token's row times the choice's weight to its place, and its dot product with
+// the row that lies there.  A token's choices are neighbours, so that its row is read from memory once.
+template <typename T, int LPR, int CH, bool FEW>
+__global__ __launch_bounds__(256) void dispatch_dot_kernel(const RowsArgs a) {
+  constexpr int GPB = 256 / LPR;
+  const int lane = threadIdx.x % LPR;
+  const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
+  for (int64_t f = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR; f < rows; f += (int64_t)gridDim.x * GPB) {
+    const int64_t p = a.place[f], t = (int)f / a.k;
+    const bool in = p >= 0 && p < held;
+    const float w = a.weights ? a.weights[f] : 1.f;
+    const T* x = reinterpret_cast<const T*>(a.x) + t * a.ldx;
+    const T* z = reinterpret_cast<const T*>(a.rows) + (in ? p : 0) * a.ldr;
+    T* y = reinterpret_cast<T*>(a.out) + p * a.ldo;
+    float dot = 0.f;
+    for (int c0 = 0; c0 < a.width; c0 += 8 * LPR * CH) {
+      Raw8<T> rx[CH], rz[CH];
+#pragma unroll
+      for (int q = 0; q < CH; ++q) rx[q] = Part<T, FEW>(c0 + 8 * (lane + LPR * q), a.width).load(x);
+#pragma unroll
+      for (int q = 0; q < CH; ++q) rz[q] = in ? Part<T, FEW>(c0 + 8 * (lane + LPR * q), a.width).load(z) : Raw8<T>{};
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        const Part<T, FEW> at(c0 + 8 * (lane + LPR * q), a.width);
+        float v[8], u[8];
+        widen8(rx[q], v);
+        widen8(rz[q], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // (beyond a row of less than eight both are 0)
+          dot = i >= at.skip ? fmaf(u[i], v[i], dot) : dot;
+          v[i] = in ? w * v[i] : 0.f;
+        }
+        if (at.any() && p >= 0 && p < rows) at.store(y, narrow8<T>(v));
+      }
+    }
+    dot = sum_of<LPR>(dot);
+    if (lane == 0) a.dots[f] = in ? dot : 0.f;
+  }
+}
+
+// 16 lanes for each token and part of its row: its choices that an expert has, in
 // their order, four rows' loads in flight at a time.
-template <typename T>
+template <typename T, bool FEW>
 __global__ __launch_bounds__(256) void combine_kernel(const RowsArgs a) {
-  const int lane = threadIdx.x & 63;
   const int64_t rows = a.tokens * a.k, held = held_rows(a, rows);
   const int parts = (a.width + kPart - 1) / kPart;
   const int64_t jobs = a.tokens * parts;
-  for (int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < jobs; job += (int64_t)gridDim.x * 4) {
-    const int64_t t = jobs >> 31 ? job / parts : (int)job / parts;
-    const int c = (int)(job - t * parts) * kPart + 8 * lane;
-    const int mine = lane < a.k ? a.place[t * a.k + lane] : -1;
-    const float weight = lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
-    uint64_t left = __ballot(mine >= 0 && mine < held);
-    float s[8];
+  for (int64_t job = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); job < jobs; job += (int64_t)gridDim.x * 16) {
+    int64_t t;
+    int part;
+    part_of(job, jobs, parts, t, part);
+    const Part<T, FEW> at(part * kPart + 8 * (int)(threadIdx.x & 15), a.width);
+    if (!at.any()) continue;
+    const int32_t* place = a.place + t * a.k;
+    const float* weight = a.weights + t * a.k;
+    float s[8] = {};
+    if (a.x) widen8(at.load(reinterpret_cast<const T*>(a.x) + t * a.ldx), s);
+    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+      int64_t p[kChoices];
+      float w[kChoices];
+      Raw8<T> r[kChoices];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = 0.f;
-    if (a.x && c < a.width) load_part<T>(reinterpret_cast<const T*>(a.x) + t * a.ldx, c, a.width, s);
-    const T* from = reinterpret_cast<const T*>(a.rows) + c;
-    if (c + 8 <= a.width) {
-      auto next = [&](float& w) {
-        const int j = __builtin_ctzll(left);
-        left &= left - 1;
-        w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
-        return load8<T>(from + __builtin_amdgcn_readlane(mine, j) * a.ldr);
-      };
-      auto add = [&](const Raw8<T>& r, float w) {
-        float u[8];
-        widen8(r, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = fmaf(w, u[i], s[i]);
-      };
-      while (__popcll(left) >= 4) {
-        Raw8<T> r[4];
-        float w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) r[q] = next(w[q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) add(r[q], w[q]);
+      for (int q = 0; q < kChoices; ++q) {
+        const int j = j0 + q < a.k ? j0 + q : j0;
+        p[q] = place[j];
+        w[q] = a.weights ? weight[j] : 1.f;
+        if (j0 + q >= a.k || p[q] >= held) p[q] = -1;
       }
-      while (left) {
-        float w;
-        const Raw8<T> r = next(w);
-        add(r, w);
-      }
-    } else if (c < a.width) {
-      for (; left; left &= left - 1) {
-        const int j = __builtin_ctzll(left);
-        const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weight), j));
-        float u[8];
-        load_part<T>(from + __builtin_amdgcn_readlane(mine, j) * a.ldr - c, c, a.width, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = fmaf(w, u[i], s[i]);
+      for (int q = 0; q < kChoices; ++q)
+        if (p[q] >= 0) r[q] = at.load(reinterpret_cast<const T*>(a.rows) + p[q] * a.ldr);
+#pragma unroll
+      for (int q = 0; q < kChoices; ++q) {
+        if (p[q] < 0) continue;
+        float u[8];
+        widen8(r[q], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(w[q], u[i], s[i]);
       }
     }
-    if (c < a.width) store_part<T>(reinterpret_cast<T*>(a.out) + t * a.ldo, c, a.width, s);
+    at.store(reinterpret_cast<T*>(a.out) + t * a.ldo, narrow8<T>(s));
   }
 }
 
 // ------------------------------------------------------------ launchers
 namespace {
 
-constexpr int64_t kMaxGroups = 1 << 16;  // workgroups along a launch's tokens; each takes every so manieth
+constexpr int64_t kMaxGroups = 1 << 16;      // workgroups of a launch over tokens; each takes every so manieth
+constexpr int64_t kMaxRowGroups = 1 << 20;   // over rows' parts
 
 template <typename T, int LPT, int Q>
 hipError_t route_go(const RouteArgs& a, hipStream_t s) {
@@ -692,20 +711,44 @@ unsigned token_groups(int64_t tokens) {
   return (unsigned)(g < kMaxGroups ? g : kMaxGroups);
 }
 
-template <typename T>
-hipError_t dispatch_go(const RowsArgs& a, hipStream_t s) {
-  constexpr int CH = sizeof(T) == 2 ? 4 : 2;
-  if (a.dots) {
-    hipLaunchKernelGGL((dispatch_dot_kernel<T>), dim3(token_groups(a.tokens)), dim3(256), 0, s, a);
-  } else {
-    const unsigned parts = (unsigned)((a.width + CH * kPart - 1) / (CH * kPart));
-    hipLaunchKernelGGL((dispatch_kernel<T>), dim3(token_groups(a.tokens), parts), dim3(256), 0, s, a);
-  }
+unsigned row_groups(int64_t jobs, int per_block) {
+  const int64_t g = (jobs + per_block - 1) / per_block;
+  return (unsigned)(g < kMaxRowGroups ? g : kMaxRowGroups);
+}
+
+template <typename T, int LPR, int CH, bool FEW = false>
+hipError_t copy_go(const RowsArgs& a, hipStream_t s) {
+  constexpr int kPiece = 8 * LPR * CH;
+  hipLaunchKernelGGL((dispatch_kernel<T, LPR, CH, FEW>), dim3(row_groups(a.tokens * ((a.width + kPiece - 1) / kPiece), 256 / LPR)),
+                     dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+template <typename T, int LPR, int CH, bool FEW = false>
+hipError_t dot_go(const RowsArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((dispatch_dot_kernel<T, LPR, CH, FEW>), dim3(row_groups(a.tokens * a.k, 256 / LPR)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <typename T>
+hipError_t dispatch_go(const RowsArgs& a, hipStream_t s) {
+  if (a.dots) {
+    if (a.width < 8) return dot_go<T, 16, 1, true>(a, s);
+    if (a.width <= 128) return dot_go<T, 16, 1>(a, s);
+    if (a.width <= 256) return dot_go<T, 16, 2>(a, s);
+    if (a.width <= 512) return dot_go<T, 16, 4>(a, s);
+    if (a.width <= 1024) return dot_go<T, 64, 2>(a, s);
+    return dot_go<T, 64, 4>(a, s);
+  }
+  if (a.width < 8) return copy_go<T, 16, 1, true>(a, s);
+  if (a.width < 1024) return copy_go<T, 16, 1>(a, s);
+  return copy_go<T, 64, sizeof(T) == 2 ? 4 : 2>(a, s);
+}
+template <typename T>
 hipError_t combine_go(const RowsArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((combine_kernel<T>), dim3(token_groups(a.tokens * ((a.width + kPart - 1) / kPart))), dim3(256), 0, s, a);
+  const unsigned groups = row_groups(a.tokens * ((a.width + kPart - 1) / kPart), 16);
+  if (a.width < 8)
+    hipLaunchKernelGGL((combine_kernel<T, true>), dim3(groups), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, false>), dim3(groups), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
