@@ -386,9 +386,16 @@ hipError_t launch_layer_norm_forward(const LayerNormArgs& a, mr_dtype dt, hipStr
   return pick_type(a, dt, false, (int)(g < kMaxBlocks ? g : kMaxBlocks), s);
 }
 
+// As many workgroups as registers let the CUs hold, where each gets four rounds of
+// rows, and 512 at least (each leaves two rows of sums to be joined).  One chunk of
+// eight columns in a thread: five to a CU (16384 x 512 bf16 with three streams: 23
+// us, with 512 workgroups 29); two: three (8000 x 4096: 65 us, with 512 71, with
+// 1024 78; 4801 x 2944: 39, 43, 46); more: two (7710 x 4352: 82, with 768 102).
 int layer_norm_backward_blocks(int64_t rows, int64_t width) {
   const int64_t g = row_groups(rows, width);
-  return (int)(g < 512 ? g : 512);
+  const int64_t held = width <= 512 ? 1280 : width <= 1024 || (width > 2048 && width <= 4096) ? 768 : 512;
+  const int64_t most = g / 4 < 512 ? 512 : g / 4 < held ? g / 4 : held;
+  return (int)(g < most ? g : most);
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormArgs& a, mr_dtype dt, int blocks, hipStream_t s) {
