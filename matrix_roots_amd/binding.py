@@ -727,23 +727,55 @@ def _current_gpu() -> int:
     return torch.cuda.current_device()
 
 
-def _clip_problem(i, g, o, code, codes, f32):
-    """Fields of a mr_clip_problem for gradient g and output o (None: in place)."""
-    if o is None:
+def _clip_lies(i, g, o):
+    """(m, n, leading dimensions) of gradient g and output o (None: in place) that are not both dense in order."""
+    if o is None or g.stride() == o.stride():
         m, n, ld = _rows_of(g)
-        return m, n, g.data_ptr(), ld, 0, 0, code | code << 32
-    if o.shape != g.shape or o.get_device() != g.get_device():
-        raise ValueError(f"output {i} does not match its gradient")
-    if o.dtype != g.dtype and o.dtype != f32:
-        raise ValueError(f"output {i} is {o.dtype}: the gradient's type or float32 is needed")
-    if g.is_contiguous() and o.is_contiguous() or g.stride() == o.stride():
-        m, n, ld = _rows_of(g)
-        ldo = ld
-    elif g.dim() == 2 and g.stride(1) == 1 and o.stride(1) == 1:
-        (m, n), ld, ldo = g.shape, g.stride(0), o.stride(0)
-    else:
+        return m, n, ld, ld
+    if g.dim() != 2 or g.stride(1) != 1 or o.stride(1) != 1:
         raise ValueError(f"output {i} must lie as its gradient does")
-    return m, n, g.data_ptr(), ld, o.data_ptr(), ldo, code | codes[o.dtype] << 32
+    return g.shape[0], g.shape[1], g.stride(0), o.stride(0)
+
+
+def _clip_problems(grads, outs):
+    """The call's mr_clip_problem records, as rows of int64 (the two types share the last).  Whole lists at a time:
+    a set of a few hundred gradients takes the host as long as the device otherwise."""
+    import torch
+
+    T = torch.Tensor
+    count = len(grads)
+    codes = {torch.float32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
+    probs = np.zeros((count, 7), dtype=np.int64)
+    lists = [grads] if outs is None else [grads, outs]
+    gpu = _current_gpu()
+    types, dense = [], []
+    for name, ts in zip(("gradient", "output"), lists):
+        if set(map(T.get_device, ts)) != {gpu}:
+            raise ValueError(f"every {name} must be on the current GPU")
+        dtypes = [t.dtype for t in ts]
+        if not codes.keys() >= set(dtypes):
+            raise ValueError(f"every {name} must be float32, float16 or bfloat16")
+        types.append([codes[d] for d in dtypes])
+        dense.append(list(map(T.is_contiguous, ts)))
+    probs[:, 0] = 1
+    probs[:, 1] = list(map(T.numel, grads))
+    probs[:, 2] = list(map(T.data_ptr, grads))
+    probs[:, 6] = types[0]
+    if outs is None:
+        probs[:, 6] *= 1 + (1 << 32)
+    else:
+        if [t.shape for t in grads] != [t.shape for t in outs]:
+            raise ValueError("outputs must have their gradients' shapes")
+        if any(o != g and o != MR_F32 for g, o in zip(*types)):
+            raise ValueError("an output is of its gradient's type or float32")
+        probs[:, 4] = list(map(T.data_ptr, outs))
+        probs[:, 6] += np.asarray(types[1], dtype=np.int64) << 32
+    if not all(map(all, dense)):
+        for i in range(count):
+            if not all(d[i] for d in dense):
+                m, n, ld, ldo = _clip_lies(i, grads[i], None if outs is None else outs[i])
+                probs[i, [0, 1, 3, 5]] = m, n, ld, ldo
+    return probs
 
 
 def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequence] = None,
@@ -761,35 +793,22 @@ def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequ
     """
     import torch
 
-    f32 = torch.float32
-    codes = {f32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
     lib = library()
     count = len(grads)
     if count == 0:
         raise ValueError("no gradients")
     if outs is not None and len(outs) != count:
         raise ValueError("one output per gradient")
-    gpu = _current_gpu()
-    fields = []
-    for i, g in enumerate(grads):
-        code = codes.get(g.dtype)
-        if code is None:
-            raise ValueError(f"gradient {i} is {g.dtype}: float32, float16 or bfloat16 is needed")
-        if g.get_device() != gpu:
-            raise ValueError(f"gradient {i} is not on the current GPU")
-        if outs is None and g.is_contiguous():
-            fields += (1, g.numel(), g.data_ptr(), 0, 0, 0, code | code << 32)
-        else:
-            fields += _clip_problem(i, g, None if outs is None else outs[i], code, codes, f32)
-    probs = (ctypes.c_int64 * len(fields))(*fields)  # of mr_clip_problem: seven of 8 bytes, the types in the last
+    probs = _clip_problems(grads, outs)
+    at = probs.ctypes.data
     dev = grads[0].device
-    need = lib.clip_gradients_batched_workspace(ctypes.addressof(probs), count)
+    need = lib.clip_gradients_batched_workspace(at, count)
     with _memory_of(stream):
         ws = _workspace(need, dev)
         norms = torch.empty(count + 1, dtype=torch.float64, device=dev)
     _in_use_here(stream, norms)
     _in_use_on(stream, ws, norms)
-    _check(lib.clip_gradients_batched(ctypes.addressof(probs), count, float(max_norm), _ptr(norms), _ptr(ws), need,
+    _check(lib.clip_gradients_batched(at, count, float(max_norm), _ptr(norms), _ptr(ws), need,
                                       _stream(stream)))
     return (norms[0], norms[1:]) if return_norms else norms[0]
 
