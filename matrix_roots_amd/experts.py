@@ -163,6 +163,7 @@ def combine_rows(y, order: ExpertOrder, weights=None, residual=None, stream=None
     dev = _device(y, *order, weights, residual)
     code = _float_code(y, "y")
     _matrix("y", y)
+    _matrix("order.place", order[1])
     tokens, width = order[1].shape[0], y.shape[1]
     experts, k = _experts_of(order, tokens)
     _same_shape("y", y, (tokens * k, width))
