@@ -77,10 +77,6 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Q times four consecutive logits of a row, from columns c, c + step, ..; -inf
-// behind its end.  All loads come before the first use and without a branch that
-// lanes take apart: lanes at the end load the row's last four and move them down (rows of one to three
-// go to all lanes, and count for the first).
 template <typename T>
 struct Raw4 {
   typedef uint32_t u __attribute__((ext_vector_type(sizeof(T))));
@@ -96,6 +92,10 @@ __device__ __forceinline__ float widen_of(const v2u& r, int i, _Float16) {
   __builtin_memcpy(&f, &h, 2);
   return (float)f;
 }
+// Q times four consecutive logits of a row, from columns c, c + step, ..; -inf
+// behind its end.  All loads come before the first use and without a branch that
+// lanes take apart: lanes at the end load the row's last four and move them down
+// (rows of one to three go to all lanes, and count for the first).
 template <typename T, int Q>
 __device__ __forceinline__ void load_logits(const T* row, int c, int step, int n, float (&v)[4 * Q]) {
   if (n >= 4) {

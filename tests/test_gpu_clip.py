@@ -96,6 +96,18 @@ def test_where_gradients_lie(dev):
     check([flat[1:]], 0.5, [torch.zeros(10003, device=dev)[3:]])
 
 
+def test_many(dev):
+    """More gradients than a launch takes, dense and in rows, and more partial sums than a workgroup adds up by itself."""
+    flat = torch.zeros(4300 * 7, device=dev)
+    flat.copy_(randn(dev, 1, 4300 * 7))
+    big = randn(dev, 2, 130 * 20, 40).to(BF)
+    rows = [big[20 * i:20 * i + 9, 3:30] for i in range(130)]
+    check([flat[7 * i:7 * i + 1 + i % 7] for i in range(4300)], 3.0)
+    check(rows, 3.0)
+    check(rows + [flat[7 * i:7 * i + 5] for i in range(4300)], 1.0)
+    check(rows, 0.7, [torch.empty(9, 31, device=dev)[:, :27] for _ in rows])
+
+
 def test_empty_and_zero(dev):
     zero = torch.zeros(50, 3, device=dev)
     check([zero], 0.0)

@@ -228,7 +228,7 @@ def order_of(experts, n):
 @pytest.mark.parametrize("tokens, k, n", [(0, 2, 5), (1, 1, 1), (1, 8, 64), (7, 3, 2), (16, 8, 64), (65, 1, 3), (129, 4, 16),
                                           (1000, 6, 255), (2048, 8, 1), (2049, 8, 64), (4096, 4, 384), (4097, 4, 900),
                                           (300, 2, 4096), (9000, 3, 2000), (8192, 8, 4096), (16384, 8, 64), (20011, 7, 17),
-                                          (100000, 8, 8), (150000, 8, 300), (3, 64, 7)])
+                                          (100000, 8, 8), (150000, 8, 300), (3, 64, 7), (300000, 4, 40), (90000, 7, 4000)])
 def test_order(dev, tokens, k, n):
     g = gen(dev, tokens + n)
     uneven = (torch.rand(tokens, k, generator=g, device=dev) ** 3 * n).int()

@@ -18,6 +18,9 @@ from matrix_roots_amd import binding as B  # noqa: E402
 from test_gpu_linear import BF, F32, H, HF, NORM_SHAPES, TINY, U, check_eight, randn, shifted, strided, within  # noqa: E402
 
 A = 90
+# rows of less than eight columns, one column past what a kernel holds, several rounds of rows in every kernel
+MORE_SHAPES = [(5, 3), (9, 7), (600, 6), (70, 9), (3, 1537), (3, 2049), (2, 6145), (2, 12289), (2600, 513), (2100, 1032),
+               (2100, 1300), (2100, 1800), (1100, 2304), (600, 4500), (600, 7000), (530, 8200), (530, 13000)]
 
 
 @pytest.fixture(scope="module")
@@ -45,7 +48,7 @@ def reference(h, w, b, eps):
 
 
 @pytest.mark.parametrize("t", [BF, HF, F32])
-@pytest.mark.parametrize("rows, width", NORM_SHAPES)
+@pytest.mark.parametrize("rows, width", NORM_SHAPES + MORE_SHAPES)
 def test_forward(dev, rows, width, t):
     x = (randn(dev, 1, rows, width).mul_(3) + 2 * randn(dev, 11, rows, 1)).to(t)
     r = randn(dev, 2, rows, width).to(t)
@@ -119,7 +122,7 @@ def grad_reference(dy, h, mean, rstd, w, dres):
 
 
 @pytest.mark.parametrize("t", [BF, HF, F32])
-@pytest.mark.parametrize("rows, width", NORM_SHAPES)
+@pytest.mark.parametrize("rows, width", NORM_SHAPES + MORE_SHAPES)
 def test_backward(dev, rows, width, t):
     h, dy, dres = (randn(dev, s, rows, width).to(t) for s in (1, 2, 3))
     h = (h.float() * 2 + 1).to(t)
