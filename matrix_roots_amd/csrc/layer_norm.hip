@@ -324,26 +324,44 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
 }
 
 // dweight and dbias from the workgroups' sums: 32 of the 2 width columns per
-// workgroup, 32 groups of lanes over every 32nd row, joined in a fixed order.
+// workgroup, 8 lanes of four columns and 128 groups of lanes over every 128th
+// row, joined in a fixed order.
 __global__ __launch_bounds__(1024) void layer_norm_join_kernel(const float* partial, int blocks, int width,
                                                                float* dweight, float* dbias) {
-  __shared__ float part[32][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-  float s = 0.f;
-  if (c < 2 * width) {
-#pragma unroll 16
-    for (int b = g; b < blocks; b += 32) s += partial[(int64_t)b * 2 * width + c];
-  }
-  part[g][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (g == 0 && c < 2 * width) {
-    float t = part[0][threadIdx.x];
+  __shared__ float part[128][33];
+  const int l = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int c = blockIdx.x * 32 + 4 * l, n = 2 * width;
+  f4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c + 4 <= n) {
+#pragma unroll 4
+    for (int b = g; b < blocks; b += 128) {
+      const v4u u = *reinterpret_cast<const v4u_any*>(partial + (int64_t)b * n + c);
 #pragma unroll
-    for (int i = 1; i < 32; ++i) t += part[i][threadIdx.x];
-    if (c < width) {
-      if (dweight) dweight[c] = t;
+      for (int i = 0; i < 4; ++i) s[i] += __uint_as_float(u[i]);
+    }
+  } else {
+    for (int b = g; b < blocks; b += 128)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (c + i < n) s[i] += partial[(int64_t)b * n + c + i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[g][4 * l + i] = s[i];
+  __syncthreads();
+  const int col = threadIdx.x & 31, h = threadIdx.x >> 5;  // 32 groups of four
+  float t = (part[4 * h][col] + part[4 * h + 1][col]) + (part[4 * h + 2][col] + part[4 * h + 3][col]);
+  __syncthreads();
+  part[h][col] = t;
+  __syncthreads();
+  const int out = blockIdx.x * 32 + col;
+  if (h == 0 && out < n) {
+    t = part[0][col];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) t += part[i][col];
+    if (out < width) {
+      if (dweight) dweight[out] = t;
     } else if (dbias) {
-      dbias[c - width] = t;
+      dbias[out - width] = t;
     }
   }
 }

@@ -122,6 +122,7 @@ __device__ __forceinline__ void load_logits(const T* row, int c, int step, int n
 #pragma unroll
     for (int i = 0; i < 4 * Q; ++i) v[i] = i < 3 ? widen(row[i < n ? i : 0]) : 0.f;
   }
+  if (Q * step == n && step > 0) return;  // whole
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -218,12 +219,14 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
           int at = upto - count;
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            if (v[i] >= tau) mine[at++] = (uint64_t)key_of(v[i]) << 32 | ~(4u * lane + 64u * (i / 4) + i % 4);
+            if (v[i] >= tau) mine[at++] = (uint64_t)__float_as_uint(v[i]) << 32 | ~(4u * lane + 64u * (i / 4) + i % 4);
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          const uint64_t own_key = lane < total ? mine[lane] : 0;
+          const uint64_t reached = mine[lane];  // of lanes behind the last one, whatever lies there
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
           place = 0;
-          const uint32_t hi = (uint32_t)(own_key >> 32), lo = (uint32_t)own_key;
+          const float value = __uint_as_float((uint32_t)(reached >> 32));
+          const uint32_t hi = lane < total ? key_of(value) : 0, lo = (uint32_t)reached;
+          const uint64_t own_key = (uint64_t)hi << 32 | lo;
           static_for<15>([&](auto r) {
             const uint64_t other = (uint64_t)ror<r.value + 1>(hi) << 32 | ror<r.value + 1>(lo);
             place += other > own_key;
@@ -231,7 +234,6 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
           if (lane >= total) place = lane;  // behind the others
           if (lane < total && place < a.k) {
             expert = (int32_t)~lo;
-            const float value = __uint_as_float((hi >> 31) ? hi ^ 0x80000000u : ~hi);
             part = expf(value - top);
           }
         }
