@@ -9,7 +9,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
+from array import array
 from typing import Optional, Sequence
 
 import numpy as np
@@ -738,44 +740,52 @@ def _clip_lies(i, g, o):
 
 
 def _clip_problems(grads, outs):
-    """The call's mr_clip_problem records, as rows of int64 (the two types share the last).  Whole lists at a time:
+    """The call's mr_clip_problem records, seven int64 each (the two types share the last).  Whole lists at a time:
     a set of a few hundred gradients takes the host as long as the device otherwise."""
     import torch
 
     T = torch.Tensor
+    types = _clip_types()
+    gpu = {_current_gpu()}
+    if set(map(T.get_device, grads)) != gpu:
+        raise ValueError("every gradient must be on the current GPU")
     count = len(grads)
-    codes = {torch.float32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
-    probs = np.zeros((count, 7), dtype=np.int64)
-    lists = [grads] if outs is None else [grads, outs]
-    gpu = _current_gpu()
-    types, dense = [], []
-    for name, ts in zip(("gradient", "output"), lists):
-        if set(map(T.get_device, ts)) != {gpu}:
-            raise ValueError(f"every {name} must be on the current GPU")
-        dtypes = [t.dtype for t in ts]
-        if not codes.keys() >= set(dtypes):
-            raise ValueError(f"every {name} must be float32, float16 or bfloat16")
-        types.append([codes[d] for d in dtypes])
-        dense.append(list(map(T.is_contiguous, ts)))
-    probs[:, 0] = 1
-    probs[:, 1] = list(map(T.numel, grads))
-    probs[:, 2] = list(map(T.data_ptr, grads))
-    probs[:, 6] = types[0]
-    if outs is None:
-        probs[:, 6] *= 1 + (1 << 32)
-    else:
+    dense = list(map(T.is_contiguous, grads))
+    keys = [t.dtype for t in grads]
+    if outs is not None:
+        if set(map(T.get_device, outs)) != gpu:
+            raise ValueError("every output must be on the current GPU")
         if [t.shape for t in grads] != [t.shape for t in outs]:
             raise ValueError("outputs must have their gradients' shapes")
-        if any(o != g and o != MR_F32 for g, o in zip(*types)):
-            raise ValueError("an output is of its gradient's type or float32")
-        probs[:, 4] = list(map(T.data_ptr, outs))
-        probs[:, 6] += np.asarray(types[1], dtype=np.int64) << 32
-    if not all(map(all, dense)):
-        for i in range(count):
-            if not all(d[i] for d in dense):
-                m, n, ld, ldo = _clip_lies(i, grads[i], None if outs is None else outs[i])
-                probs[i, [0, 1, 3, 5]] = m, n, ld, ldo
+        dense = [g and o for g, o in zip(dense, map(T.is_contiguous, outs))]
+        keys = zip(keys, [t.dtype for t in outs])
+    try:
+        codes = array("q", [types[k] for k in keys])
+    except KeyError as e:
+        raise ValueError(f"{e}: gradients are float32, float16 or bfloat16, outputs alike or float32") from None
+    probs = array("q", bytes(56 * count))
+    probs[0::7] = array("q", [1]) * count
+    probs[1::7] = array("q", map(T.numel, grads))
+    probs[2::7] = array("q", map(T.data_ptr, grads))
+    if outs is not None:
+        probs[4::7] = array("q", map(T.data_ptr, outs))
+    probs[6::7] = codes
+    if not all(dense):
+        for i, d in enumerate(dense):
+            if not d:
+                probs[7 * i], probs[7 * i + 1], probs[7 * i + 3], probs[7 * i + 5] = _clip_lies(
+                    i, grads[i], None if outs is None else outs[i])
     return probs
+
+
+@functools.lru_cache(maxsize=None)
+def _clip_types() -> dict:
+    """{a gradient's type, or (its type, its output's): the record's last eight bytes}"""
+    import torch
+
+    codes = {torch.float32: MR_F32, torch.float16: MR_F16, torch.bfloat16: MR_BF16}
+    pairs = {(g, o): codes[g] | codes[o] << 32 for g in codes for o in (g, torch.float32)}
+    return {**pairs, **{g: pairs[g, g] for g in codes}}
 
 
 def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequence] = None,
@@ -800,7 +810,7 @@ def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequ
     if outs is not None and len(outs) != count:
         raise ValueError("one output per gradient")
     probs = _clip_problems(grads, outs)
-    at = probs.ctypes.data
+    at = probs.buffer_info()[0]
     dev = grads[0].device
     need = lib.clip_gradients_batched_workspace(at, count)
     with _memory_of(stream):
@@ -808,8 +818,10 @@ def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequ
         norms = torch.empty(count + 1, dtype=torch.float64, device=dev)
     _in_use_here(stream, norms)
     _in_use_on(stream, ws, norms)
+    # the current stream's handle without a Stream object around it, where torch gives it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) if stream is None else None
     _check(lib.clip_gradients_batched(at, count, float(max_norm), _ptr(norms), _ptr(ws), need,
-                                      _stream(stream)))
+                                      raw(dev.index) if raw is not None else _stream(stream)))
     return (norms[0], norms[1:]) if return_norms else norms[0]
 
 
