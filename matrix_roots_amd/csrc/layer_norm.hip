@@ -27,20 +27,26 @@ namespace mr {
 
 namespace {
 
-// Sums of two values over the row's threads, in each of them.
+// Sums of two values over the row's threads, in each of them; the rows of a workgroup take their turns together.
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& u, float& v, float (*red)[16]) {
   u = sum64(u);
   v = sum64(v);
   if constexpr (TPR == 64) return;
-  const int wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6, first = threadIdx.x / TPR * (TPR / 64);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) red[0][wave] = u, red[1][wave] = v;
   __syncthreads();
-  u = red[0][0], v = red[1][0];
+  u = red[0][first], v = red[1][first];
 #pragma unroll
-  for (int w = 1; w < TPR / 64; ++w) u += red[0][w], v += red[1][w];
+  for (int w = 1; w < TPR / 64; ++w) u += red[0][first + w], v += red[1][first + w];
 }
+
+// Threads of the gradient's workgroups: four rows of one wave, two of four waves that
+// hold more than two chunks (7710 x 4352 bf16 74 us, one row at a time 82; 969 x 6503
+// 26 and 33: half as many sums to join), else one.
+template <int TPR, int CH>
+constexpr int kBackThreads = TPR == 256 && CH > 2 ? 512 : kNormThreads<TPR>;
 
 // The eight columns a thread holds of a row in chunk k of CH.  Chunks before the
 // last are whole (`pick` takes the smallest CH).  In that one the thread at a ragged
@@ -206,10 +212,10 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
 // and of dy into a.partial[2 blockIdx.x] and the row behind it.  Rows stay as they
 // are stored until they are used, which leaves registers for the next row's loads.
 template <typename T, int TPR, int CH, bool FEW>
-__global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(const LayerNormArgs a) {
-  constexpr int RPB = kNormThreads<TPR> / TPR, NV = 8;
+__global__ __launch_bounds__((kBackThreads<TPR, CH>)) void layer_norm_backward_kernel(const LayerNormArgs a) {
+  constexpr int RPB = kBackThreads<TPR, CH> / TPR, NV = 8;
   __shared__ float red[2][16];
-  __shared__ float cols[RPB > 1 ? 2 * TPR * CH * NV : 1];
+  __shared__ float cols[RPB > 1 ? TPR * CH * NV : 1];
   int t = RPB == 1 ? (int)threadIdx.x : (int)threadIdx.x % TPR;  // place among the row's threads
   const float inv_width = 1.f / (float)a.width;
   float dw[CH][NV], db[CH][NV];
@@ -220,8 +226,9 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
   Raw8<T> dy[CH], h[CH];
   float rho = 0.f, mu = 0.f;
   const int64_t step = (int64_t)gridDim.x * RPB;
-  // the next row's loads are under way while one is worked on, but for the widest of float32, which takes all registers
-  constexpr bool kAhead = sizeof(T) == 2 || TPR < 512;
+  // the next row's loads are under way while one is worked on, but for float32 in four chunks of 512 threads, which take
+  // all registers
+  constexpr bool kAhead = sizeof(T) == 2 || TPR == 64 || CH < 4;
   auto span = [&](int k) { return Span<TPR, CH, FEW>(t, k, a.width); };
   auto load = [&](int64_t r) {
     const T* from_dy = reinterpret_cast<const T*>(a.dy) + r * a.lddy;
@@ -234,8 +241,19 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
     }
   };
   int64_t r = (int64_t)blockIdx.x * RPB + (RPB == 1 ? 0 : threadIdx.x / TPR);
-  if (r < a.rows) load(r);
-  while (r < a.rows) {  // whole waves (RPB > 1) or the whole workgroup: the barriers below come after the loop
+  auto ahead = [&](int64_t r) {
+    if (r < a.rows) {
+      load(r);
+    } else {  // no row: nothing to the sums
+      rho = mu = 0.f;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) dy[k] = h[k] = Raw8<T>{};
+    }
+  };
+  ahead(r);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += step, r += step) {
+    const bool on = r < a.rows;
+    if (TPR == 64 && !on) break;  // whole waves; the barriers below come after the loop
     asm volatile("" : "+v"(t));  // columns and addresses are worked out per row, not kept in registers over the loop
     float sg = 0.f, dot = 0.f;
     Raw8<T> now_dy[CH], now_h[CH], rr[CH];
@@ -244,9 +262,9 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       now_dy[k] = dy[k], now_h[k] = h[k];
-      if (res) rr[k] = span(k).load(res);
+      if (res && on) rr[k] = span(k).load(res);
     }
-    if (kAhead && r + step < a.rows) load(r + step);
+    if (kAhead) ahead(r + step);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float w[NV], g[NV], hh[NV];
@@ -289,30 +307,32 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_backward_kernel(
       if (res) widen8(rr[k], u);
 #pragma unroll
       for (int i = 0; i < NV; ++i) u[i] += now_rho * (g[i] * w[i] - c0 - (hh[i] - now_mu) * now_rho * c1);
-      span(k).store(dx, u);
+      if (on) span(k).store(dx, u);
     }
-    if (!kAhead && r + step < a.rows) load(r + step);
-    r += step;
+    if (!kAhead) ahead(r + step);
   }
   if (!a.partial) return;
   float* out = a.partial + 2 * (int64_t)blockIdx.x * a.width;
   if constexpr (RPB > 1) {
-    constexpr int B = TPR * CH * NV;
-    for (int w = 1; w < RPB; ++w) {  // waves 1, 2, 3 add to wave 0's sums in turn
+    auto join = [&](float (&s)[CH][NV], int w) {  // the wth rows' threads add to the first's
+      __syncthreads();
       if ((int)threadIdx.x / TPR == w) {
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
-          for (int i = 0; i < NV; ++i) cols[(k * NV + i) * TPR + t] = dw[k][i], cols[B + (k * NV + i) * TPR + t] = db[k][i];
+          for (int i = 0; i < NV; ++i) cols[(k * NV + i) * TPR + t] = s[k][i];
       }
       __syncthreads();
       if ((int)threadIdx.x < TPR) {
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
-          for (int i = 0; i < NV; ++i) dw[k][i] += cols[(k * NV + i) * TPR + t], db[k][i] += cols[B + (k * NV + i) * TPR + t];
+          for (int i = 0; i < NV; ++i) s[k][i] += cols[(k * NV + i) * TPR + t];
       }
-      __syncthreads();
+    };
+    for (int w = 1; w < RPB; ++w) {
+      join(dw, w);
+      join(db, w);
     }
     if ((int)threadIdx.x >= TPR) return;
   }
@@ -374,7 +394,7 @@ constexpr int kMaxBlocks = 2048;  // 8 workgroups per CU
 template <typename T, int TPR, int CH, bool FEW = false>
 hipError_t go(const LayerNormArgs& a, bool backward, int blocks, hipStream_t s) {
   if (backward)
-    hipLaunchKernelGGL((layer_norm_backward_kernel<T, TPR, CH, FEW>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
+    hipLaunchKernelGGL((layer_norm_backward_kernel<T, TPR, CH, FEW>), dim3(blocks), dim3(kBackThreads<TPR, CH>), 0, s, a);
   else
     hipLaunchKernelGGL((layer_norm_forward_kernel<T, TPR, CH, FEW>), dim3(blocks), dim3(kNormThreads<TPR>), 0, s, a);
   return hipGetLastError();
@@ -411,14 +431,16 @@ hipError_t launch_layer_norm_forward(const LayerNormArgs& a, mr_dtype dt, hipStr
 }
 
 // As many workgroups as registers let the CUs hold, where each gets four rounds of
-// rows, and 512 at least (each leaves two rows of sums to be joined).  One chunk of
-// eight columns in a thread: five to a CU (16384 x 512 bf16 with three streams: 23
-// us, with 512 workgroups 29); two: three (8000 x 4096: 65 us, with 512 71, with
-// 1024 78; 4801 x 2944: 39, 43, 46); more: two (7710 x 4352: 82, with 768 102).
+// rows, and the least of those at least (each leaves two rows of sums to be joined).
+// One chunk of eight columns in a thread: five to a CU (16384 x 512 bf16 with three
+// streams: 23 us, with 512 workgroups 29); two: three (8000 x 4096: 65 us, with 512 71,
+// with 1024 78; 4801 x 2944: 38, 43, 46); more: two, or one of twice the threads.
 int layer_norm_backward_blocks(int64_t rows, int64_t width) {
-  const int64_t g = row_groups(rows, width);
-  const int64_t held = width <= 512 ? 1280 : width <= 1024 || (width > 2048 && width <= 4096) ? 768 : 512;
-  const int64_t most = g / 4 < 512 ? 512 : g / 4 < held ? g / 4 : held;
+  const bool two = width > 4096 && width <= 8192;  // rows at a time of 512 threads
+  const int64_t g = two ? (rows + 1) / 2 : row_groups(rows, width);
+  const int64_t held = width <= 512 ? 1280 : width <= 1024 || (width > 2048 && width <= 4096) ? 768 : two ? 256 : 512;
+  const int64_t least = two ? 256 : 512;
+  const int64_t most = g / 4 < least ? least : g / 4 < held ? g / 4 : held;
   return (int)(g < most ? g : most);
 }
 
