@@ -17,7 +17,7 @@
 //
 // HBM-bound.  16384 x 2048 bf16: forward with residual and y 49 us from a clean cache
 // (268 MB, 5.4 TB/s), 58 in passes one after another; gradient with the residual's
-// 57.5 us (278 MB, 4.8 TB/s) and 5.0 for the join of its columns' sums.  A row
+// 54 us (278 MB, 5.2 TB/s) and 4.9 for the join of its columns' sums.  A row
 // belongs to one wave (up to 2048 columns) or to the waves of a workgroup (up to
 // 16384), in as few chunks of eight columns a thread as hold it.
 #include "mr_common.hpp"

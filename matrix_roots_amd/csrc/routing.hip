@@ -163,8 +163,7 @@ __device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]
 // tau (equal values), and for more choices, one is chosen after another: the
 // largest, its first place, which is then taken out.  16384 tokens of 384 float32
 // logits, k = 8: 12.5 us, one after another 18.0.
-// Bound by its vector instructions, about 800 for a wave of four tokens: the waves
-// of a batch are all resident and load at once (25 MB, 5 us), then compare.
+// The waves of a batch are all resident: they load at once (25 MB, 5 us), then compare.
 template <typename T, int LPT, int Q>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
   constexpr int TPB = 256 / LPT, N = 4 * Q;
