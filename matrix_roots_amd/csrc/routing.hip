@@ -158,17 +158,23 @@ __device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]
 //
 // Up to eight choices by 16 lanes: with tau the k-th largest of the lanes' own
 // largest logits, k of a token's logits at least reach tau, so all chosen ones do.
-// They are few (about 11 of 384 for k = 8), go to LDS, one to each lane, and each
-// finds its place by comparing itself with the others.  Where more than 16 reach
-// tau (equal values), and for more choices, one is chosen after another: the
-// largest, its first place, which is then taken out.  16384 tokens of 384 float32
-// logits, k = 8: 12.5 us, one after another 18.0.
-// The waves of a batch are all resident: they load at once (25 MB, 5 us), then compare.
+// They are few, go to LDS, and each finds its place by comparing itself with the
+// others.  Where more reach tau than there is room for (many are equal), and for
+// more choices, one is chosen after another: the largest, its first place, which is
+// then taken out.
+//
+// Room for 16, one in each lane, up to 128 logits, for 32, two in each, above.  Of 384
+// and k = 8, 10.5 reach tau in the mean and more than 16 once in 110 tokens; the few
+// waves that choose one after another for it end behind all others.  Of 128 logits
+// that is rare, and the second one's registers halve the resident waves.
+// 16384 x 384 float32, k = 8: 12.5 us with room for 16, 9.3 for 32, 18.0 all one after
+// another (25 MB, 5 us, in one burst of loads before the comparisons).  65536 x 128,
+// k = 4: 12.9 with room for 16, 15 for 32.
 template <typename T, int LPT, int Q>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
-  constexpr int TPB = 256 / LPT, N = 4 * Q;
+  constexpr int TPB = 256 / LPT, N = 4 * Q, kReach = Q <= 2 ? 16 : 32;
   constexpr float kInf = __builtin_inff();
-  __shared__ uint64_t reach[LPT == 16 ? TPB : 1][16];
+  __shared__ uint64_t reach[LPT == 16 ? TPB : 1][kReach];
   const int lane = threadIdx.x % LPT;
   for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < a.tokens; t0 += (int64_t)gridDim.x * TPB) {
     // lanes behind the last token work on that one and store nothing
@@ -193,9 +199,9 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
       sum = sum_of<LPT>(sum);
     }
     // of this lane: one of the chosen, which one of them, its share before the division
-    int32_t expert = -1;
-    int place = lane;
-    float part = 0.f;
+    int32_t expert = -1, second = -1;
+    int place = lane, second_place = kMaxRouted;
+    float part = 0.f, second_part = 0.f;
     bool done = false;
     if constexpr (LPT == 16) {
       if (a.k <= 8) {
@@ -212,7 +218,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
         upto += shr<4>(upto);
         upto += shr<8>(upto);
         const int total = over<16>((uint32_t)upto, [](uint32_t x, uint32_t y) { return umax(x, y); });
-        done = !__any(total > 16);
+        done = !__any(total > kReach);
         if (done) {
           uint64_t* mine = reach[threadIdx.x / 16];
           int at = upto - count;
@@ -220,16 +226,31 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
           for (int i = 0; i < N; ++i)
             if (v[i] >= tau) mine[at++] = (uint64_t)__float_as_uint(v[i]) << 32 | ~(4u * lane + 64u * (i / 4) + i % 4);
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          const uint64_t reached = mine[lane];  // of lanes behind the last one, whatever lies there
+          // of lanes behind the last one, whatever lies there
+          const uint64_t one = mine[lane], two = mine[kReach - 16 + lane];
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          const float value = __uint_as_float((uint32_t)(one >> 32)), value2 = __uint_as_float((uint32_t)(two >> 32));
+          const uint32_t lo = (uint32_t)one, hi = lane < total ? key_of(value) : 0;
+          const uint64_t key = (uint64_t)hi << 32 | lo;
           place = 0;
-          const float value = __uint_as_float((uint32_t)(reached >> 32));
-          const uint32_t hi = lane < total ? key_of(value) : 0, lo = (uint32_t)reached;
-          const uint64_t own_key = (uint64_t)hi << 32 | lo;
           static_for<15>([&](auto r) {
-            const uint64_t other = (uint64_t)ror<r.value + 1>(hi) << 32 | ror<r.value + 1>(lo);
-            place += other > own_key;
+            place += ((uint64_t)ror<r.value + 1>(hi) << 32 | ror<r.value + 1>(lo)) > key;
           });
+          if (kReach > 16 && __any(total > 16)) {  // some lanes hold two
+            const uint32_t lo2 = (uint32_t)two, hi2 = 16 + lane < total ? key_of(value2) : 0;
+            const uint64_t key2 = (uint64_t)hi2 << 32 | lo2;
+            place += key2 > key;
+            second_place = key > key2;
+            static_for<15>([&](auto r) {
+              const uint64_t other2 = (uint64_t)ror<r.value + 1>(hi2) << 32 | ror<r.value + 1>(lo2);
+              place += other2 > key;
+              second_place += (((uint64_t)ror<r.value + 1>(hi) << 32 | ror<r.value + 1>(lo)) > key2) + (other2 > key2);
+            });
+            if (hi2 && second_place < a.k) {
+              second = (int32_t)~lo2;
+              second_part = expf(value2 - top);
+            }
+          }
           if (lane >= total) place = lane;  // behind the others
           if (lane < total && place < a.k) {
             expert = (int32_t)~lo;
@@ -256,11 +277,15 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
         }
       }
     }
-    if (a.normalize) sum = sum_of<LPT>(part);
+    if (a.normalize) sum = sum_of<LPT>(part + second_part);
     if (!held) continue;
     if (place < a.k) {
       a.experts[t * a.k + place] = expert;
       a.weights[t * a.k + place] = expert < 0 ? 0.f : part / sum;
+    }
+    if (second >= 0) {
+      a.experts[t * a.k + second_place] = second;
+      a.weights[t * a.k + second_place] = second_part / sum;
     }
     if (lane == 0) a.log_sum[t] = top == -kInf ? top : top + logf(sum);
   }

@@ -90,6 +90,29 @@ def test_route_ties_go_to_the_lowest(dev, experts, k):
         check_route(logits.to(t), k, False)
 
 
+@pytest.mark.parametrize("experts", [64, 128, 250, 256, 384, 512])
+@pytest.mark.parametrize("k", [3, 8])
+def test_route_many_that_reach(dev, experts, k):
+    """Each count of logits that reach the k-th of the lanes' largest, from k to 60:
+    they stand in the columns of k lanes of 16, one of which holds the lowest alone."""
+    g = torch.Generator().manual_seed(experts + k)
+    rows = []
+    for count in range(k, 61):
+        lanes = torch.randperm(16, generator=g)[:k].tolist()
+        of = [[c for c in range(experts) if c // 4 % 16 == lane] for lane in lanes]
+        row = torch.rand(experts, generator=g) - 5.0
+        row[of[0][0]] = 4.0
+        rest = [c for one in of[1:] for c in one[1:]]
+        more = [one[0] for one in of[1:]] + [rest[i] for i in torch.randperm(len(rest), generator=g).tolist()]
+        at = more[: count - 1]
+        row[at] = 4.0 + torch.rand(len(at), generator=g)
+        rows.append(row)
+    logits = torch.stack(rows).to(dev)
+    for t in (F32, HF, BF):
+        for normalize in (True, False):
+            check_route(logits.to(t), k, normalize)
+
+
 @pytest.mark.parametrize("experts, k", [(8, 3), (64, 8), (300, 16), (700, 5)])
 def test_route_masked(dev, experts, k):
     """Experts at -inf and at the type's lowest value; tokens with fewer than k experts, with one, with none."""
