@@ -188,7 +188,8 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
     }
     row_sum2<TPR>(ds, ss, red);
     const float e = ds * inv_width;
-    const float rho = 1.f / sqrtf(fmaxf(fmaf(-e, e, ss * inv_width), 0.f) + a.eps);
+    const float var = fmaf(-e, e, ss * inv_width);
+    const float rho = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);  // NaN stays NaN
     if (t == 0) {
       if (a.mean) a.mean[r] = m + e;
       if (a.rstd) a.rstd[r] = rho;
