@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void layer_norm_forward_kernel(c
     const float var = fmaf(-e, e, ss * inv_width);
     const float rho = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);  // NaN stays NaN
     if (t == 0) {
-      if (a.mean) a.mean[r] = m + e;
+      if (a.mean) a.mean[r] = __builtin_isinf(m) ? m : m + e;  // an infinite m: differences are no numbers
       if (a.rstd) a.rstd[r] = rho;
     }
 #pragma unroll

@@ -38,3 +38,17 @@ def test_rows_that_hold_no_numbers(dev, width, t):
         assert torch.equal(g[~bad], e[~bad])
     dx = mr.layer_norm_backward(dy, out.h, out.mean, out.rstd, w)[0]
     assert bool(dx[bad].isnan().all()) and torch.equal(dx[~bad], clean_dx[~bad])
+
+
+@pytest.mark.parametrize("t", [BF, HF, F32])
+@pytest.mark.parametrize("width", [1, 3, 500, 1337, 5000, 9000])
+def test_mean_of_rows_that_hold_infinity(dev, width, t):
+    """Infinities of one sign: that infinity; of both, or with a NaN beside them: NaN."""
+    inf = math.inf
+    x = randn(dev, 1, 6, width).to(t)
+    x[1, 0], x[3, width // 2], x[4, 0], x[5, width - 1] = inf, -inf, inf, math.nan
+    x[4, width - 1] = -inf
+    mean = mr.layer_norm_forward(x, torch.ones(width, device=dev), None, 1e-5).mean
+    want = x.double().mean(1)
+    assert bool((mean.isnan() == want.isnan()).all()) and bool((mean.isinf() == want.isinf()).all())
+    assert mean[1] == inf and mean[3] == -inf and bool(torch.isfinite(mean[[0, 2]]).all())
