@@ -52,3 +52,29 @@ def test_mean_of_rows_that_hold_infinity(dev, width, t):
     want = x.double().mean(1)
     assert bool((mean.isnan() == want.isnan()).all()) and bool((mean.isinf() == want.isinf()).all())
     assert mean[1] == inf and mean[3] == -inf and bool(torch.isfinite(mean[[0, 2]]).all())
+
+
+def rows_of_exact_sums(rows, width):
+    """Rows of eight-bit numbers times 256 below 2^16 in size, signs in turn, whose groups of eight columns add up to
+    zero, but for column 7: one to 253, odd.  A row's sum is below 2^17, odd beside multiples of four, and no sum on the
+    way to it, however the groups are joined, takes more than 24 bits."""
+    g = torch.Generator().manual_seed(width)
+    a = torch.randint(129, 255, (rows, width // 2), generator=g).double()
+    step = torch.tensor([1.0, -1.0]).double().repeat(width // 4)
+    x = torch.stack([a, -(a + step)], 2).view(rows, width) * 256
+    x[:, 7] = torch.randint(0, 64, (rows,), generator=g).double() * 4 + 1
+    return x
+
+
+@pytest.mark.parametrize("t, width", [(BF, 1024), (BF, 2048), (BF, 4096), (BF, 8192), (BF, 16384), (HF, 1024), (HF, 2048), (HF, 4096)])
+def test_mean_of_16_bit_rows(dev, width, t):
+    """The exact mean, a float32, comes out as it is.  Differences of the row's values from a number of the row's own
+    type are multiples of its last place: 2^17 over 2^-6 (bf16, 16384 columns: means from two on) or over 2^-7 (fp16,
+    4096 columns: from eight on) is 2^24 at most, so they and their sums are exact.  Differences from a float32 mean
+    take up to 2^16 over 2^-10 and would all be rounded the same way, by 2^-10."""
+    x = rows_of_exact_sums(40, width)
+    want = x.mean(1)
+    assert torch.equal(want.float().double(), want) and torch.equal(x.to(t).double(), x)
+    out = mr.layer_norm_forward(x.to(t).to(dev), torch.ones(width, device=dev), None, 1e-5)
+    got = out.mean.cpu().double()
+    assert torch.equal(got, want), float((got - want).abs().max())
