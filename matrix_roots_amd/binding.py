@@ -707,7 +707,8 @@ def _rows_of(t):
     dense."""
     if t.is_contiguous():
         return 1, t.numel(), 0
-    dims = sorted(((st, n) for st, n in zip(t.stride(), t.shape) if n != 1), reverse=True)
+    # (a dimension of one value and unit stride makes rows of one value: a column of a matrix)
+    dims = sorted(((st, n) for st, n in zip(t.stride(), t.shape) if n != 1 or st == 1), reverse=True)
     if dims[-1][0] != 1:
         raise ValueError("gradients need a dimension of unit stride")
     m, n, ld = 1, 1, 0

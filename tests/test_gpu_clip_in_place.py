@@ -81,3 +81,25 @@ def test_no_gradients(dev):
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
     assert lib.clip_gradients_batched(at, 3, 1.0, norms.data_ptr(), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
     assert norms.tolist() == [0.0] * 4
+
+
+@pytest.mark.parametrize("t", [F32, BF])
+def test_columns(dev, t):
+    """Columns of a matrix, in place and into outputs: the values around them stay."""
+    big = torch.full((700, 9), 3.0, dtype=t, device=dev)
+    kept = torch.full((41, 5, 3), 3.0, dtype=t, device=dev)
+    grads = [big[:, 4:5], kept[:, :, 1:2]]
+    for i, g in enumerate(grads):
+        g.copy_(randn(dev, i, *g.shape))
+    before = [g.double() for g in grads]
+    n = float(sum(b.square().sum() for b in before).sqrt())
+    rel = 300 * 2.0 ** -52
+    for into in ([torch.zeros(700, 1, device=dev)], None):
+        part = grads[:1] if into is not None else grads
+        limit = 0.5 * (float(before[0].square().sum().sqrt()) if into is not None else n)
+        norm = float(mr.clip_gradients_batched(part, limit, outs=into))
+        assert abs(norm - 2 * limit) <= norm * rel
+        for g, b in zip(into or part, before):
+            within(g, b * 0.5, b.abs() * 0.5 * (H[g.dtype] * 1.01 + U + 2 * rel) + TINY[g.dtype])
+    assert bool((big[:, :4] == 3).all()) and bool((big[:, 5:] == 3).all())
+    assert bool((kept[:, :, 0] == 3).all()) and bool((kept[:, :, 2] == 3).all())
