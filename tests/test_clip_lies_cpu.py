@@ -23,3 +23,12 @@ def test_columns_and_dense_outputs():
     assert B._clip_lies(0, big[:, 4:5], torch.zeros(6, 1)) == (6, 1, 16, 1)
     assert B._clip_lies(0, big[:, 4:5], big[:, 5:6]) == (6, 1, 16, 16)
     assert B._clip_lies(0, big[:, 4:5], None) == (6, 1, 16, 16)
+
+
+def test_strides_of_single_values_do_not_matter():
+    """A dimension of one value may have any stride: the tensors lie alike all the same."""
+    a, b = torch.zeros(5, 14, 7)[:, :1], torch.zeros(5, 98).as_strided((5, 1, 7), (98, 98, 1))
+    assert a.stride() != b.stride()
+    assert B._clip_lies(0, a, b) == (5, 7, 98, 98)
+    with pytest.raises(ValueError):
+        B._clip_lies(0, a, torch.zeros(5, 1, 7))
