@@ -439,7 +439,9 @@ hipError_t launch_layer_norm_forward(const LayerNormArgs& a, mr_dtype dt, hipStr
 // rows, and the least of those at least (each leaves two rows of sums to be joined).
 // One chunk of eight columns in a thread: five to a CU (16384 x 512 bf16 with three
 // streams: 23 us, with 512 workgroups 29); two: three (8000 x 4096: 65 us, with 512 71,
-// with 1024 78; 4801 x 2944: 38, 43, 46); more: two, or one of twice the threads.
+// with 1024 78; 4801 x 2944: 38, 43, 46; rows of one wave, 16384 x 1024: 34, with 512
+// 37, with 1280 41; 16384 x 768: 30, 33, 37; float32 alone does better with 512, 51
+// against 53 at 16384 x 1024); more: two, or one of twice the threads.
 int layer_norm_backward_blocks(int64_t rows, int64_t width) {
   const bool two = width > 4096 && width <= 8192;  // rows at a time of 512 threads
   const int64_t g = two ? (rows + 1) / 2 : row_groups(rows, width);

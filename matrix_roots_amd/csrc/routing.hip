@@ -163,13 +163,22 @@ __device__ __forceinline__ void store4(T* row, int c, int n, const float (&v)[4]
 // more choices, one is chosen after another: the largest, its first place, which is
 // then taken out.
 //
-// Room for 16, one in each lane, up to 128 logits, for 32, two in each, above.  Of 384
-// and k = 8, 10.5 reach tau in the mean and more than 16 once in 110 tokens; the few
-// waves that choose one after another for it end behind all others.  Of 128 logits
-// that is rare, and the second one's registers halve the resident waves.
-// 16384 x 384 float32, k = 8: 12.5 us with room for 16, 9.3 for 32, 18.0 all one after
-// another (25 MB, 5 us, in one burst of loads before the comparisons).  65536 x 128,
-// k = 4: 12.9 with room for 16, 15 for 32.
+// Room for 16, one in each lane, up to 128 logits, for 32, two in each, above.  How
+// many reach tau depends on k more than on the number of experts.  k = 8: 10.5 in the
+// mean of 384 normal logits, 10.2 of 128; more than 16 for one token in 125 and one in
+// 280, and the few waves that choose one after another for it end behind all others.
+// k = 4: 4.4, and more than 16 for none.  Among a few dozen experts the lanes that hold
+// any are few, and tau low: of 40 logits 5% of the tokens have more than 16 for k = 8, of
+// 32 37%, of 17 to 28 all of them.  None of 200000 tokens of up to 512 had more than 32.
+// In a captured graph, float32, with room for 16 / for 32 / one after another:
+//   16384 x 384, k = 8   13.5 /  9.9 / 15.5 us (25 MB, 5 us, in one burst of loads before the comparisons)
+//   65536 x 128, k = 4   12.8 / 15.0 / 14.5    (the second place's registers halve the resident waves)
+//   65536 x 128, k = 8   15.0 / 16.1 / 21.8
+//   16384 x 128, k = 8    7.4 /  6.4 /  8.3    (fewer waves than the card holds: they cost nothing)
+//   65536 x 64,  k = 8   12.1 / 13.2 / 17.9
+//   16384 x 32,  k = 8    7.6 /  7.0 /  7.0
+// k = 16, one after another: 16384 x 384 25 us.  k = 8 beyond: 16384 x 512 13 us; one after
+// another by 64 lanes 16384 x 513 and x 1024 34, x 2048 59 (134 MB), 4096 x 4096 44.
 template <typename T, int LPT, int Q>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
   constexpr int TPB = 256 / LPT, N = 4 * Q, kReach = Q <= 2 ? 16 : 32;
