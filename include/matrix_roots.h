@@ -593,7 +593,9 @@ mr_status rms_norm_backward(const mr_rms_norm_grad_problem* problem, void* ws, s
  * w_dtype (weight, bias): dtype or MR_F32.  bias may be NULL (none).  h is
  * required with a residual and ignored without one; mean, rstd, y and q (with
  * scales, MR_BLOCK_VECTOR) are each written where not NULL, at least one of y
- * and q.
+ * and q.  A row that holds NaN or infinity has an rstd of NaN and the mean that its
+ * sum gives.  Sums are float32: a row whose sum overflows is taken for such a row, one
+ * whose squares about the mean do has an rstd of 0.
  */
 typedef struct {
   int64_t rows, width;

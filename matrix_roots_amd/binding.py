@@ -796,11 +796,12 @@ def clip_gradients_batched(grads: Sequence, max_norm: float, outs: Optional[Sequ
     either case then.
 
     grads: float32, float16 or bfloat16 tensors on the current GPU, of any shape,
-    whose values lie in rows one stride apart; outs: tensors of the same shapes
-    that lie alike, of the gradient's type or float32 (as gram_ema_update takes
-    them).  No two may share the bytes between their first and last values.
-    Returns n, a float64 device scalar; with return_norms (n, norms), the
-    gradients' own norms.  max_norm math.inf: the norms alone.
+    whose values lie in rows of unit stride, one stride apart (columns are rows of
+    one value); outs: tensors of the same shapes that lie alike, of the gradient's
+    type or float32 (as gram_ema_update takes them).  No two may share the bytes
+    between their first and last values.  Returns n, a float64 device scalar;
+    with return_norms (n, norms), the gradients' own norms.  max_norm math.inf: the
+    norms alone.
     """
     import torch
 
