@@ -78,3 +78,15 @@ def test_mean_of_16_bit_rows(dev, width, t):
     out = mr.layer_norm_forward(x.to(t).to(dev), torch.ones(width, device=dev), None, 1e-5)
     got = out.mean.cpu().double()
     assert torch.equal(got, want), float((got - want).abs().max())
+
+
+@pytest.mark.parametrize("width", [100, 1337, 5000])
+def test_rows_beyond_the_range_of_sums(dev, width):
+    """A sum that overflows: as a row with infinity; squares that do: a deviation's reciprocal of 0."""
+    x = torch.full((3, width), 3e38, device=dev)
+    x[1], x[2] = 1.0, 1e21
+    x[2, ::2] = -1e21
+    out = mr.layer_norm_forward(x, torch.ones(width, device=dev), None, 1e-5)
+    assert out.mean[0] == math.inf and bool(out.rstd[0].isnan()) and bool(out.y[0].isnan().all())
+    assert out.mean[1] == 1 and bool((out.y[1] == 0).all())
+    assert out.rstd[2] == 0 and bool((out.y[2] == 0).all())
